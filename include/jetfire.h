@@ -81,7 +81,8 @@ typedef enum {
   JF_ERR_TIMEOUT = -7, /* reported by jf_device_status: a kernel's bounded wait ran out */
   JF_ERR_DEVICE = -8,  /* no usable sm_100 device is current */
   JF_ERR_WORKSPACE = -9, /* the caller's workspace is NULL, misaligned or smaller than required */
-  JF_ERR_ARG = -10       /* an enumerated argument (jf_granularity) is unknown */
+  JF_ERR_ARG = -10,      /* an enumerated or scalar argument is unknown or out of range */
+  JF_ERR_RANGE = -11     /* reported by jf_device_status: a position lay outside the rotary table */
 } jf_status;
 
 /* Scale granularity of the quantizer variants (f3): one fp32 scale per 32x32 block ([rows/32,
@@ -238,6 +239,130 @@ JF_API int64_t jf_layernorm_i8_bwd_workspace_bytes(int64_t rows, int64_t cols);
 JF_API int jf_layernorm_i8_bwd_noalloc(jf_cqtensor X, jf_cqtensor dY, const float* gamma, float eps,
                                        jf_qtensor dX, float* dgamma, float* dbeta, void* stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * A transformer block around the linear layer. The pages describe the INT8 data flow of the linear and
+ * non-linear operators and leave attention in 16 bits (summary, "Approach" and "Limitations"); these calls
+ * add what a whole block needs next to them: biases, activations and residual joins inside the linear
+ * layers, the biases' gradients, and the way from the INT8 QKV projection to dense attention inputs and
+ * back. They have no counterpart on the pages.
+ * ------------------------------------------------------------------------------------------------ */
+
+/* Activations: RELU max(x, 0); GELU x Phi(x); GELU_TANH 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3)));
+ * SILU x / (1 + exp(-x)). The derivative of RELU at 0 is taken as 0. */
+typedef enum { JF_ACT_NONE = 0, JF_ACT_RELU = 1, JF_ACT_GELU = 2, JF_ACT_GELU_TANH = 3, JF_ACT_SILU = 4 } jf_activation;
+
+/* Dense row-major matrices whose rows start ld elements apart (device pointers; p = NULL: absent).
+ * p and the row pitch in bytes are multiples of 16, ld is at least the number of columns. */
+typedef struct {
+  const void* p;
+  jf_dtype dt;
+  int64_t ld;
+} jf_cmatrix;
+typedef struct {
+  void* p;
+  jf_dtype dt;
+  int64_t ld;
+} jf_matrix;
+
+/*
+ * Linear forward with bias, activation and residual in its epilogue:
+ *   P = X W^T + bias,  Z = act(P) + R        (X [M, K], W [N, K], Z [M, N])
+ * in fp32 from jf_linear_fwd's accumulators; nothing but the outputs reaches memory.
+ *   bias  device fp32 [N], 16-byte aligned, or NULL
+ *   Rq/R  the residual: an INT8 tensor (Rq.q) or a dense matrix (R.p), at most one of them (JF_ERR_ARG)
+ *   Y     optional output: requant(Z) per 32x32 block (Y.q = NULL to skip it)
+ *   y     optional output: Z rounded once to y.dt. At least one of Y and y is required (JF_ERR_NULL).
+ *   P     optional output: requant(P), what the backward of the activation needs (P.q = NULL to skip it)
+ * K = 0 gives Z = act(bias) + R. Outputs must not overlap inputs or each other (JF_ERR_ALIAS; matrices by
+ * the whole range from their first to their last element), with one exception: y may be R itself (same
+ * pointer, dtype and ld), which updates a residual stream in place.
+ */
+JF_API int jf_linear_fwd_epilogue(jf_cqtensor X, jf_cqtensor W, const float* bias, jf_activation act, jf_cqtensor Rq,
+                                  jf_cmatrix R, jf_qtensor Y, jf_matrix y, jf_qtensor P, void* stream);
+
+/*
+ * Input gradient with the activation's derivative and a residual gradient in its epilogue:
+ *   Z = (dY W) * act'(P) + R                 (dY [M, N], W [N, K], Z [M, K])
+ *   P     the INT8 pre-activation [M, K] that the forward saved (act'(fp32(P.q) P.s)); required unless act
+ *         is JF_ACT_NONE, when it is not read
+ *   Rq/R, Y, y as above. The residual is what reached the linear's input along the other branch.
+ */
+JF_API int jf_linear_dgrad_epilogue(jf_cqtensor dY, jf_cqtensor W, jf_cqtensor P, jf_activation act, jf_cqtensor Rq,
+                                    jf_cmatrix R, jf_qtensor Y, jf_matrix y, void* stream);
+
+/*
+ * Bias gradient: db[n] = sum_m fp32(dY.q[m, n]) dY.s[m/32, n/32] in fp32 (deterministic: a fixed order).
+ *   db  device fp32 [N], 4-byte aligned. M = 0 gives zeros.
+ */
+JF_API int jf_bias_grad(jf_cqtensor dY, float* db, void* stream);
+
+/* Pairs that a rotation turns: (j, j + rot_dim/2), or (2j, 2j + 1). */
+typedef enum { JF_ROPE_HALF = 0, JF_ROPE_INTERLEAVED = 1 } jf_rope_layout;
+
+/*
+ * Rotary tables: cos_table[p, j] = magnitude cos(p inv_freq[j]) and sin_table likewise, p in [0, length),
+ * angles formed in fp64 and rounded once. Position scalings for long contexts are choices of inv_freq and
+ * magnitude.
+ *   inv_freq  HOST array of `half` doubles (read during the call); half in [1, 128]
+ *   cos_table, sin_table  device fp32 [length, half], 16-byte aligned (outputs)
+ */
+JF_API int jf_rope_table(const double* inv_freq, int64_t half, double magnitude, int64_t length, float* cos_table,
+                         float* sin_table, void* stream);
+
+/* Heads of a QKV tensor [rows, (q_heads + 2 kv_heads) head_dim]: columns are the q heads, then the k heads,
+ * then the v heads; row batch * seq + s is token s of a sequence; rows past batch * seq are padding. */
+typedef struct {
+  int64_t batch, seq;
+  int64_t q_heads, kv_heads;  /* either may be 0 */
+  int64_t head_dim;           /* a multiple of 32, at most 256 */
+  int64_t rot_dim;            /* leading dimensions that rotate: a multiple of 16, at most head_dim; 0: none */
+  jf_rope_layout layout;
+  const float *cos_table, *sin_table; /* device fp32 [table_len, rot_dim / 2], 16-byte aligned */
+  int64_t table_len;
+  const int64_t* positions;   /* device [batch * seq], or NULL: token s is at position s (seq <= table_len) */
+  const float *gamma_q, *gamma_k; /* RMS norm weights, device fp32 [head_dim], 16-byte aligned; NULL: no norm */
+  float eps;                  /* > 0 */
+} jf_qkv_rope;
+
+/* Dense heads: dimension 0 of (batch b, token s, head h) is at p + b stride_b + s stride_s + h stride_h
+ * (elements); the dimensions are contiguous. p and every stride (in bytes) are multiples of 16. */
+typedef struct {
+  const void* p;
+  int64_t stride_b, stride_s, stride_h;
+} jf_cheads;
+typedef struct {
+  void* p;
+  int64_t stride_b, stride_s, stride_h;
+} jf_heads;
+
+/*
+ * Queries, keys and values of an INT8 QKV tensor, of type dt: per head u = x rsqrt(mean(x^2) + eps) gamma
+ * (x = fp32(q) s; u = x without a gamma) and the first rot_dim dimensions of u rotated by the token's angle;
+ * values are x. All in fp32, rounded once. Padding rows are not read and nothing is written for them.
+ *   q, k, v  outputs. Views of one buffer are allowed; they must not overlap each other (not checked) or an
+ *            input (checked). The strides of an output must not map two of its elements to one place
+ *            (JF_ERR_SHAPE).
+ * A position outside the table gives NaN in the rotated dimensions of its token, and JF_ERR_RANGE from the
+ * next jf_device_status.
+ */
+JF_API int jf_qkv_rope_fwd(jf_cqtensor QKV, const jf_qkv_rope* a, jf_heads q, jf_heads k, jf_heads v, jf_dtype dt,
+                           void* stream);
+
+/*
+ * Its gradient: from dq, dk, dv (type dt; strides of 0 broadcast) to dQKV, re-quantized per 32x32 block over
+ * the valid rows (padding rows get codes 0), and the norm weights' gradients (fp32 [head_dim], deterministic).
+ *   dgamma_q, dgamma_k  nullable; each needs its gamma (JF_ERR_NULL). When either is given, `workspace` must
+ *       hold jf_qkv_rope_bwd_workspace_bytes(rows, a) bytes (16-byte aligned, JF_ERR_WORKSPACE). Calls that
+ *       may run at the same time, two captured graphs among them, need workspaces of their own.
+ * QKV is read only where there is a norm. A position outside the table gives a zero gradient in the rotated
+ * dimensions before the norm, and JF_ERR_RANGE from the next jf_device_status.
+ */
+JF_API int jf_qkv_rope_bwd(jf_cqtensor QKV, const jf_qkv_rope* a, jf_cheads dq, jf_cheads dk, jf_cheads dv, jf_dtype dt,
+                           jf_qtensor dQKV, float* dgamma_q, float* dgamma_k, void* workspace, int64_t workspace_bytes,
+                           void* stream);
+/* Bytes of that workspace for a QKV tensor of `rows` rows, or -1 for invalid arguments. */
+JF_API int64_t jf_qkv_rope_bwd_workspace_bytes(int64_t rows, const jf_qkv_rope* a);
+
 /*
  * The plain INT8 tensor-core product C = A B^T with an int32 result and no scales (no counterpart
  * on the pages: it measures the tensor core's INT8 rate, the ceiling the block-scaled GEMMs above
@@ -313,7 +438,8 @@ JF_API const char* jf_strerror(int status);
 /*
  * Synchronizes `stream`, then returns and clears the device-side status of the library on the
  * current device: JF_OK, or JF_ERR_TIMEOUT if a kernel gave up a bounded wait since the last
- * call (its outputs are then undefined), or JF_ERR_CUDA if the synchronization failed.
+ * call (its outputs are then undefined), or JF_ERR_RANGE if one met a position outside its rotary table,
+ * or JF_ERR_CUDA if the synchronization failed.
  */
 JF_API int jf_device_status(void* stream);
 

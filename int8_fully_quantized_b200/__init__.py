@@ -13,6 +13,7 @@ A quantized tensor is a pair ``QTensor(q, s)``: ``q`` int8 [rows, cols] codes an
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import NamedTuple, Optional
 
@@ -23,7 +24,7 @@ from .build_lib import LIB_PATH
 
 __all__ = [
     "QTensor", "JetfireError", "load_library", "empty_qtensor", "EXPORTED_SYMBOLS", "JF_F32", "JF_BF16", "JF_F16",
-    "GRANULARITY",
+    "GRANULARITY", "ACTIVATIONS", "ROPE_LAYOUTS", "QKVRope",
     # C ABI, one wrapper per entry point
     "jf_quantize_block", "jf_dequantize_block", "jf_linear_fwd", "jf_linear_fwd_gelu", "jf_linear_dgrad",
     "jf_linear_wgrad", "jf_gelu_i8", "jf_layernorm_i8", "jf_gelu_i8_bwd", "jf_layernorm_i8_bwd",
@@ -31,14 +32,18 @@ __all__ = [
     "jf_layernorm_i8_bwd_workspace_bytes", "jf_layernorm_i8_bwd_noalloc", "jf_quantize_granular",
     "jf_dequantize_granular", "jf_quantization_error", "jf_granular_scale_count", "jf_mx_quantize",
     "jf_mx_linear_fwd", "jf_gemm_i8_s32", "jf_selftest_wait_timeout", "jf_strerror",
-    "jf_device_status", "jf_sm_count",
+    "jf_device_status", "jf_sm_count", "jf_linear_fwd_epilogue", "jf_linear_dgrad_epilogue", "jf_bias_grad",
+    "jf_rope_table", "jf_qkv_rope_fwd", "jf_qkv_rope_bwd", "jf_qkv_rope_bwd_workspace_bytes",
     # allocating helpers
     "quantize_block", "dequantize_block", "linear_fwd", "linear_fwd_gelu", "linear_dgrad", "linear_wgrad",
     "gelu_i8", "layernorm_i8", "gelu_i8_bwd", "layernorm_i8_bwd", "quantize_granular", "quantization_mse",
-    "mx_quantize", "mx_linear_fwd",
+    "mx_quantize", "mx_linear_fwd", "linear_fwd_epilogue", "linear_dgrad_epilogue", "bias_grad", "rope_frequencies",
+    "rope_table", "qkv_rope", "qkv_rope_bwd",
 ]
 
 JF_F32, JF_BF16, JF_F16 = 0, 1, 2
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 GRANULARITY = {"block": 0, "token": 1, "channel": 2, "tensor": 3}
 _DTYPES = {torch.float32: JF_F32, torch.bfloat16: JF_BF16, torch.float16: JF_F16}
 
@@ -48,6 +53,8 @@ EXPORTED_SYMBOLS = (
     "jf_gelu_i8", "jf_layernorm_i8", "jf_gelu_i8_bwd", "jf_layernorm_i8_bwd", "jf_layernorm_i8_bwd_workspace_bytes",
     "jf_layernorm_i8_bwd_noalloc", "jf_quantize_granular", "jf_dequantize_granular", "jf_quantization_error",
     "jf_granular_scale_count", "jf_mx_quantize", "jf_mx_linear_fwd", "jf_gemm_i8_s32", "jf_selftest_wait_timeout",
+    "jf_linear_fwd_epilogue", "jf_linear_dgrad_epilogue", "jf_bias_grad", "jf_rope_table", "jf_qkv_rope_fwd",
+    "jf_qkv_rope_bwd", "jf_qkv_rope_bwd_workspace_bytes",
     "jf_strerror",
     "jf_device_status",
     "jf_sm_count",
@@ -60,6 +67,23 @@ class _CQ(ctypes.Structure):
 
 class _Q(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class _Matrix(ctypes.Structure):   # jf_cmatrix and jf_matrix
+    _fields_ = [("p", ctypes.c_void_p), ("dt", ctypes.c_int), ("ld", ctypes.c_int64)]
+
+
+class _Heads(ctypes.Structure):    # jf_cheads and jf_heads
+    _fields_ = [("p", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_s", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
+
+
+class _Rope(ctypes.Structure):     # jf_qkv_rope
+    _fields_ = [("batch", ctypes.c_int64), ("seq", ctypes.c_int64), ("q_heads", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64), ("rot_dim", ctypes.c_int64),
+                ("layout", ctypes.c_int), ("cos_table", ctypes.c_void_p), ("sin_table", ctypes.c_void_p),
+                ("table_len", ctypes.c_int64), ("positions", ctypes.c_void_p), ("gamma_q", ctypes.c_void_p),
+                ("gamma_k", ctypes.c_void_p), ("eps", ctypes.c_float)]
 
 
 class JetfireError(RuntimeError):
@@ -105,6 +129,14 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.jf_mx_linear_fwd.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp]
     lib.jf_gemm_i8_s32.argtypes = [vp, vp, vp, i64, i64, i64, vp]
     lib.jf_selftest_wait_timeout.argtypes = [i64, vp]
+    lib.jf_linear_fwd_epilogue.argtypes = [_CQ, _CQ, vp, i32, _CQ, _Matrix, _Q, _Matrix, _Q, vp]
+    lib.jf_linear_dgrad_epilogue.argtypes = [_CQ, _CQ, _CQ, i32, _CQ, _Matrix, _Q, _Matrix, vp]
+    lib.jf_bias_grad.argtypes = [_CQ, vp, vp]
+    lib.jf_rope_table.argtypes = [ctypes.POINTER(ctypes.c_double), i64, ctypes.c_double, i64, vp, vp, vp]
+    rope = ctypes.POINTER(_Rope)
+    lib.jf_qkv_rope_fwd.argtypes = [_CQ, rope, _Heads, _Heads, _Heads, i32, vp]
+    lib.jf_qkv_rope_bwd.argtypes = [_CQ, rope, _Heads, _Heads, _Heads, i32, _Q, vp, vp, vp, i64, vp]
+    lib.jf_qkv_rope_bwd_workspace_bytes.argtypes = [i64, rope]
     lib.jf_strerror.argtypes = [i32]
     lib.jf_strerror.restype = ctypes.c_char_p
     lib.jf_device_status.argtypes = [vp]
@@ -114,6 +146,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
             getattr(lib, name).restype = ctypes.c_int
     lib.jf_layernorm_i8_bwd_workspace_bytes.restype = i64
     lib.jf_granular_scale_count.restype = i64
+    lib.jf_qkv_rope_bwd_workspace_bytes.restype = i64
     _lib = lib
     return lib
 
@@ -340,6 +373,226 @@ def jf_gemm_i8_s32(a: torch.Tensor, b: torch.Tensor, c: torch.Tensor, stream=Non
     _check(lib.jf_gemm_i8_s32(_ptr(a), _ptr(b), _ptr(c), M, N, K, _stream(stream)), "jf_gemm_i8_s32")
 
 
+# ---- a transformer block around the linear layer: epilogues, bias gradient, QKV norm and rotation
+class _On:
+    """Makes the device of the tensors of a call current for its duration, after checking that they share one."""
+
+    def __init__(self, *tensors):
+        self.guard = None
+        device = None
+        for t in tensors:
+            for u in (t if isinstance(t, QTensor) else (t,)):
+                if u is None:
+                    continue
+                if device is None:
+                    device = u.device
+                elif u.device != device:
+                    raise ValueError(f"tensors on {device} and {u.device} in one call")
+        if device is None or not torch.cuda.is_available():
+            return   # without a GPU the call refuses by itself
+        if device.type != "cuda":
+            raise ValueError(f"tensors on {device}: the kernels take device memory")
+        if device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _q_checked(t: Optional[QTensor], what: str):
+    if t is not None:
+        if t.q.dtype != torch.int8 or t.s.dtype != torch.float32:
+            raise ValueError(f"{what}: codes must be int8 and scales float32")
+        if t.q.dim() != 2 or tuple(t.s.shape) != (t.q.shape[0] // 32, t.q.shape[1] // 32):
+            raise ValueError(f"{what}: scales of shape {tuple(t.s.shape)} do not belong to codes of shape {tuple(t.q.shape)}")
+    return t
+
+
+def _f32_vector(t: Optional[torch.Tensor], n: int, what: str) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or tuple(t.shape) != (n,):
+        raise ValueError(f"{what} must be float32 of shape ({n},), got {t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def _matrix(t: Optional[torch.Tensor], rows: int, cols: int, what: str) -> _Matrix:
+    """A dense matrix whose rows may be strided (the last dimension is contiguous)."""
+    if t is None:
+        return _Matrix(None, 0, cols)
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{what}: unsupported dtype {t.dtype}")
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{what} must have shape ({rows}, {cols}), got {tuple(t.shape)}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    return _Matrix(t.data_ptr() if t.numel() else None, _DTYPES[t.dtype], t.stride(0) if rows > 1 else max(cols, 1))
+
+
+_NO_CQ, _NO_Q = _CQ(None, None, 0, 0), _Q(None, None, 0, 0)
+
+
+def _residual(residual, rows: int, cols: int):
+    if isinstance(residual, QTensor):
+        return _cq(_q_checked(residual, "residual")), _matrix(None, rows, cols, "residual")
+    return _NO_CQ, _matrix(residual, rows, cols, "residual")
+
+
+def _activation(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+def jf_linear_fwd_epilogue(X: QTensor, W: QTensor, Y: Optional[QTensor] = None, y: Optional[torch.Tensor] = None,
+                           bias: Optional[torch.Tensor] = None, act: str = "none", residual=None,
+                           P: Optional[QTensor] = None, stream=None) -> None:
+    """Z = act(X W^T + bias) + residual into Y (INT8 blocks) and / or y (dense fp32, bf16 or fp16, rows may be
+    strided); P receives the re-quantized pre-activation. The residual is a QTensor or a dense matrix; y
+    may be the dense residual itself."""
+    lib = load_library()
+    for t, what in ((X, "X"), (W, "W"), (Y, "Y"), (P, "P")):
+        _q_checked(t, what)
+    rows, cols = X.rows, W.rows
+    Rq, R = _residual(residual, rows, cols)
+    with _On(X, W, Y, y, bias, residual, P):
+        _check(lib.jf_linear_fwd_epilogue(_cq(X), _cq(W), _f32_vector(bias, cols, "bias"), _activation(act), Rq, R,
+                                          _NO_Q if Y is None else _q(Y, rows, cols), _matrix(y, rows, cols, "y"),
+                                          _NO_Q if P is None else _q(P, rows, cols), _stream(stream)),
+               "jf_linear_fwd_epilogue")
+
+
+def jf_linear_dgrad_epilogue(dY: QTensor, W: QTensor, dX: Optional[QTensor] = None, dx: Optional[torch.Tensor] = None,
+                             pre: Optional[QTensor] = None, act: str = "none", residual=None, stream=None) -> None:
+    """Z = (dY W) * act'(pre) + residual into dX (INT8 blocks) and / or dx (dense); pre is the INT8
+    pre-activation the forward saved."""
+    lib = load_library()
+    for t, what in ((dY, "dY"), (W, "W"), (dX, "dX"), (pre, "pre")):
+        _q_checked(t, what)
+    rows, cols = dY.rows, W.cols
+    Rq, R = _residual(residual, rows, cols)
+    with _On(dY, W, dX, dx, pre, residual):
+        _check(lib.jf_linear_dgrad_epilogue(_cq(dY), _cq(W), _NO_CQ if pre is None else _cq(pre), _activation(act), Rq, R,
+                                            _NO_Q if dX is None else _q(dX, rows, cols), _matrix(dx, rows, cols, "dx"),
+                                            _stream(stream)), "jf_linear_dgrad_epilogue")
+
+
+def jf_bias_grad(dY: QTensor, db: torch.Tensor, stream=None) -> None:
+    """db (float32 [cols]) = the column sums of dY."""
+    lib = load_library()
+    _q_checked(dY, "dY")
+    with _On(dY, db):
+        _check(lib.jf_bias_grad(_cq(dY), _f32_vector(db, dY.cols, "db"), _stream(stream)), "jf_bias_grad")
+
+
+def jf_rope_table(inv_freq, cos: torch.Tensor, sin: torch.Tensor, magnitude: float = 1.0, stream=None) -> None:
+    """Fills the float32 tables cos and sin [length, len(inv_freq)] of the angles position * inv_freq[j]."""
+    lib = load_library()
+    half = len(inv_freq)
+    for t, what in ((cos, "cos"), (sin, "sin")):
+        if t.dtype != torch.float32 or t.dim() != 2 or t.shape[1] != half or t.shape != cos.shape:
+            raise ValueError(f"{what} must be float32 of shape (length, {half})")
+    freq = (ctypes.c_double * max(half, 1))(*[float(f) for f in inv_freq])
+    with _On(cos, sin):
+        _check(lib.jf_rope_table(freq, half, float(magnitude), cos.shape[0], _ptr(cos), _ptr(sin), _stream(stream)),
+               "jf_rope_table")
+
+
+class QKVRope(NamedTuple):
+    """Heads, rotary tables and norm weights of a QKV tensor (struct jf_qkv_rope). The INT8 tensor's columns
+    are q_heads, then kv_heads key and kv_heads value heads of head_dim columns; row b * seq + s is token s of
+    sequence b, rows past batch * seq are padding. cos and sin are [table_len, rot_dim / 2] (see rope_table);
+    positions, int64 with batch * seq elements, defaults to each token's place in its sequence."""
+    batch: int
+    seq: int
+    q_heads: int
+    kv_heads: int
+    head_dim: int
+    cos: Optional[torch.Tensor] = None
+    sin: Optional[torch.Tensor] = None
+    positions: Optional[torch.Tensor] = None
+    gamma_q: Optional[torch.Tensor] = None
+    gamma_k: Optional[torch.Tensor] = None
+    eps: float = 1e-6
+    layout: str = "half"
+
+
+def _rope(a: QKVRope) -> _Rope:
+    if a.layout not in ROPE_LAYOUTS:
+        raise ValueError(f"unknown layout {a.layout!r}: one of {', '.join(ROPE_LAYOUTS)}")
+    if (a.cos is None) != (a.sin is None):
+        raise ValueError("cos and sin belong together")
+    half = length = 0
+    if a.cos is not None:
+        if a.cos.dtype != torch.float32 or a.sin.dtype != torch.float32 or a.cos.dim() != 2 or a.cos.shape != a.sin.shape:
+            raise ValueError("cos and sin must be float32 tables of one shape (length, rot_dim / 2)")
+        length, half = a.cos.shape
+    if a.positions is not None and (a.positions.dtype != torch.int64 or a.positions.numel() != a.batch * a.seq):
+        raise ValueError(f"positions must be int64 with {a.batch * a.seq} elements")
+    return _Rope(a.batch, a.seq, a.q_heads, a.kv_heads, a.head_dim, 2 * half, ROPE_LAYOUTS[a.layout],
+                 None if a.cos is None else _ptr(a.cos), None if a.sin is None else _ptr(a.sin), length,
+                 None if a.positions is None else _ptr(a.positions), _f32_vector(a.gamma_q, a.head_dim, "gamma_q"),
+                 _f32_vector(a.gamma_k, a.head_dim, "gamma_k"), a.eps)
+
+
+def _heads(t: Optional[torch.Tensor], a: QKVRope, heads: int, heads_first: bool, dtype, what: str) -> _Heads:
+    if t is None:
+        if heads * a.batch * a.seq:
+            raise ValueError(f"{what} is missing")
+        return _Heads(None, 0, 0, 0)
+    shape = (a.batch, heads, a.seq, a.head_dim) if heads_first else (a.batch, a.seq, heads, a.head_dim)
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be {dtype} of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    if t.stride(3) != 1 and t.numel():
+        raise ValueError(f"{what}: the last dimension must be contiguous")
+    b, x, y = t.stride(0), t.stride(1), t.stride(2)
+    return _Heads(t.data_ptr() if t.numel() else None, b, y if heads_first else x, x if heads_first else y)
+
+
+def jf_qkv_rope_fwd(qkv: QTensor, a: QKVRope, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+                    v: Optional[torch.Tensor], heads_first: bool = False, stream=None) -> None:
+    """q, k and v ([batch, seq, heads, head_dim], with heads_first [batch, heads, seq, head_dim]; strided views
+    allowed) of the INT8 tensor qkv, queries and keys normed per head and rotated."""
+    lib = load_library()
+    _q_checked(qkv, "qkv")
+    given = [t for t in (q, k, v) if t is not None]
+    dtype = given[0].dtype if given else torch.float32
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    t = [_heads(x, a, n, heads_first, dtype, w) for x, n, w in ((q, a.q_heads, "q"), (k, a.kv_heads, "k"), (v, a.kv_heads, "v"))]
+    with _On(qkv, q, k, v, a.cos, a.sin, a.positions, a.gamma_q, a.gamma_k):
+        _check(lib.jf_qkv_rope_fwd(_cq(qkv), ctypes.byref(_rope(a)), *t, _DTYPES[dtype], _stream(stream)), "jf_qkv_rope_fwd")
+
+
+def jf_qkv_rope_bwd_workspace_bytes(rows: int, a: QKVRope) -> int:
+    return int(load_library().jf_qkv_rope_bwd_workspace_bytes(rows, ctypes.byref(_rope(a))))
+
+
+def jf_qkv_rope_bwd(qkv: QTensor, a: QKVRope, dq, dk, dv, dqkv: QTensor, dgamma_q: Optional[torch.Tensor] = None,
+                    dgamma_k: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    heads_first: bool = False, stream=None) -> None:
+    """The gradient of jf_qkv_rope_fwd: dq, dk, dv to INT8 dqkv and the norm weights' gradients."""
+    lib = load_library()
+    _q_checked(qkv, "qkv")
+    _q_checked(dqkv, "dqkv")
+    given = [t for t in (dq, dk, dv) if t is not None]
+    dtype = given[0].dtype if given else torch.float32
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    t = [_heads(x, a, n, heads_first, dtype, w) for x, n, w in ((dq, a.q_heads, "dq"), (dk, a.kv_heads, "dk"), (dv, a.kv_heads, "dv"))]
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _On(qkv, dq, dk, dv, dqkv, dgamma_q, dgamma_k, workspace, a.cos, a.sin, a.positions, a.gamma_q, a.gamma_k):
+        _check(lib.jf_qkv_rope_bwd(_cq(qkv), ctypes.byref(_rope(a)), *t, _DTYPES[dtype], _q(dqkv, qkv.rows, qkv.cols),
+                                   _f32_vector(dgamma_q, a.head_dim, "dgamma_q"),
+                                   _f32_vector(dgamma_k, a.head_dim, "dgamma_k"), _ptr(workspace), nbytes,
+                                   _stream(stream)), "jf_qkv_rope_bwd")
+
+
 def jf_selftest_wait_timeout(limit_ns: int, stream=None) -> None:
     lib = load_library()
     _check(lib.jf_selftest_wait_timeout(limit_ns, _stream(stream)), "jf_selftest_wait_timeout")
@@ -444,3 +697,101 @@ def layernorm_i8_rowstats(X: QTensor, stats: torch.Tensor, gamma: torch.Tensor, 
     Y = empty_qtensor(X.rows, X.cols, X.q.device)
     jf_layernorm_i8_rowstats(X, stats, gamma, beta, eps, Y, stream)
     return Y
+
+
+def linear_fwd_epilogue(X: QTensor, W: QTensor, bias: Optional[torch.Tensor] = None, act: str = "none", residual=None,
+                        want_pre: bool = False, out_dtype: Optional[torch.dtype] = None, stream=None):
+    """act(X W^T + bias) + residual as INT8 blocks, or as a dense matrix of out_dtype; with ``want_pre`` also
+    the re-quantized pre-activation X W^T + bias, for linear_dgrad_epilogue. The residual is a QTensor or a
+    dense matrix of any supported dtype."""
+    dev = X.q.device
+    Y = empty_qtensor(X.rows, W.rows, dev) if out_dtype is None else None
+    y = torch.empty((X.rows, W.rows), dtype=out_dtype, device=dev) if out_dtype is not None else None
+    P = empty_qtensor(X.rows, W.rows, dev) if want_pre else None
+    jf_linear_fwd_epilogue(X, W, Y, y, bias, act, residual, P, stream)
+    out = Y if y is None else y
+    return (out, P) if want_pre else out
+
+
+def linear_dgrad_epilogue(dY: QTensor, W: QTensor, pre: Optional[QTensor] = None, act: str = "none", residual=None,
+                          out_dtype: Optional[torch.dtype] = None, stream=None):
+    """(dY W) * act'(pre) + residual as INT8 blocks, or as a dense matrix of out_dtype."""
+    dev = dY.q.device
+    dX = empty_qtensor(dY.rows, W.cols, dev) if out_dtype is None else None
+    dx = torch.empty((dY.rows, W.cols), dtype=out_dtype, device=dev) if out_dtype is not None else None
+    jf_linear_dgrad_epilogue(dY, W, dX, dx, pre, act, residual, stream)
+    return dX if dx is None else dx
+
+
+def bias_grad(dY: QTensor, stream=None) -> torch.Tensor:
+    """The bias gradient (float32 [cols]): the column sums of the INT8 gradient dY."""
+    db = torch.empty(dY.cols, dtype=torch.float32, device=dY.q.device)
+    jf_bias_grad(dY, db, stream)
+    return db
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_length: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(inv_freq, magnitude) of rotary positions over rot_dim dimensions, for rope_table.
+
+    scaling "none": f_j = base^(-2 j / rot_dim). "linear": positions divided by ``factor``. "ntk": the base
+    raised to base * factor^(rot_dim / (rot_dim - 2)), which leaves the fastest frequency and divides the
+    slowest by ``factor``. "yarn": frequencies that turn more than beta_fast times over original_length stay,
+    those that turn less than beta_slow times are divided by ``factor``, a linear ramp over j between; the
+    tables are multiplied by 0.1 ln(factor) + 1."""
+    if rot_dim <= 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be positive and even")
+    if scaling not in ("none", "linear", "ntk", "yarn"):
+        raise ValueError(f"unknown scaling {scaling!r}: one of none, linear, ntk, yarn")
+    if factor <= 0.0 or (scaling == "ntk" and rot_dim == 2):
+        raise ValueError("factor must be positive (and ntk needs rot_dim above 2)")
+    half = rot_dim // 2
+    if scaling == "ntk":
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    freq = [base ** (-2.0 * j / rot_dim) for j in range(half)]
+    if scaling == "linear":
+        return [f / factor for f in freq], 1.0
+    if scaling == "yarn":
+        if original_length <= 0 or not beta_fast > beta_slow > 0:
+            raise ValueError("yarn needs original_length > 0 and beta_fast > beta_slow > 0")
+
+        def index_of(turns: float) -> float:   # the j whose frequency turns that often over original_length
+            return half * math.log(original_length / (2.0 * math.pi * turns)) / math.log(base)
+
+        low, high = max(math.floor(index_of(beta_fast)), 0), min(math.ceil(index_of(beta_slow)), rot_dim - 1)
+        ramp = [min(max((j - low) / max(high - low, 1e-3), 0.0), 1.0) for j in range(half)]
+        return [f * (1.0 - r) + f / factor * r for f, r in zip(freq, ramp)], 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    return freq, 1.0
+
+
+def rope_table(length: int, inv_freq, magnitude: float = 1.0, device="cuda", stream=None):
+    """(cos, sin): the float32 tables [length, len(inv_freq)] of a program's rotary positions, kept for all calls."""
+    cos = torch.empty((length, len(inv_freq)), dtype=torch.float32, device=device)
+    sin = torch.empty_like(cos)
+    jf_rope_table(inv_freq, cos, sin, magnitude, stream)
+    return cos, sin
+
+
+def qkv_rope(qkv: QTensor, a: QKVRope, dtype: torch.dtype = torch.bfloat16, heads_first: bool = False, stream=None):
+    """(q, k, v) for attention from the INT8 output of the QKV projection, [batch, seq, heads, head_dim] (with
+    heads_first [batch, heads, seq, head_dim]): queries and keys normed per head (where ``a`` has weights) and
+    rotated, values dequantized."""
+    out = [torch.empty((a.batch, n, a.seq, a.head_dim) if heads_first else (a.batch, a.seq, n, a.head_dim), dtype=dtype,
+                       device=qkv.q.device) for n in (a.q_heads, a.kv_heads, a.kv_heads)]
+    jf_qkv_rope_fwd(qkv, a, *out, heads_first, stream)
+    return tuple(out)
+
+
+def qkv_rope_bwd(qkv: QTensor, a: QKVRope, dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor, heads_first: bool = False,
+                 stream=None):
+    """(dqkv, dgamma_q, dgamma_k) of qkv_rope: an INT8 gradient for the projection's backward, and the norm
+    weights' gradients (None where there is no norm). The workspace is allocated here, per call."""
+    dev = qkv.q.device
+    dqkv = empty_qtensor(qkv.rows, qkv.cols, dev)
+    dgq = torch.empty(a.head_dim, dtype=torch.float32, device=dev) if a.gamma_q is not None else None
+    dgk = torch.empty(a.head_dim, dtype=torch.float32, device=dev) if a.gamma_k is not None else None
+    ws = None
+    if dgq is not None or dgk is not None:
+        ws = torch.empty(max(jf_qkv_rope_bwd_workspace_bytes(qkv.rows, a), 0), dtype=torch.uint8, device=dev)
+    jf_qkv_rope_bwd(qkv, a, dq, dk, dv, dqkv, dgq, dgk, ws, heads_first, stream)
+    return dqkv, dgq, dgk

@@ -25,7 +25,7 @@ NVTX_LIB_PATH = os.path.join(PKG_DIR, "libjetfire_nvtx.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-              "-shared", "--expt-relaxed-constexpr"]
+              "-shared", "--expt-relaxed-constexpr", "--threads", "0"]
 
 
 def _nvcc() -> str:
@@ -55,7 +55,7 @@ def source_hash() -> str:
 
 
 # Files that define the block-scaled GEMM kernel's device code (its host launcher lives in gemm.cu too).
-GEMM_KERNEL_FILES = ("gemm.cu", "ptx.cuh", "quant.cuh", "act.cuh")
+GEMM_KERNEL_FILES = ("gemm.cu", "epilogue.cuh", "ptx.cuh", "quant.cuh", "act.cuh")
 
 
 def kernel_source_hash(names=GEMM_KERNEL_FILES) -> str:

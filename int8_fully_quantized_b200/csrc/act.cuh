@@ -1,5 +1,6 @@
 // Device-side activation functions shared by the standalone non-linear kernels and the GEMM epilogue.
 #pragma once
+#include "kernels.h"  // GemmAct
 #include "quant.cuh"  // fma_x2
 
 namespace jf {
@@ -63,6 +64,39 @@ __device__ __forceinline__ void gelu_grad_pair_f32(float x, float& at_pos, float
   const float xc = x * 0.39894228040143267794f;
   at_pos = fmaf(xc, ex, 0.5f * (2.0f - e));
   at_neg = fmaf(-xc, ex, 0.5f * e);
+}
+
+// gelu_f32 of two values, the erfc chains packed (bit-identical to two gelu_f32 calls).
+__device__ __forceinline__ void gelu_f32_x2(float& x0, float& x1) {
+  float e0, e1;
+  erfc_nonneg_x2(fabsf(x0) * 0.70710678118654752440f, fabsf(x1) * 0.70710678118654752440f, e0, e1);
+  x0 = 0.5f * x0 * (x0 >= 0.0f ? 2.0f - e0 : e0);
+  x1 = 0.5f * x1 * (x1 >= 0.0f ? 2.0f - e1 : e1);
+}
+
+// SiLU(x) = x / (1 + exp(-x)). exp overflows to infinity for very negative x, where the quotient is 0.
+__device__ __forceinline__ float silu_f32(float x) { return __fdividef(x, 1.0f + expf(-x)); }
+
+// The tanh form of GELU, 0.5 x (1 + tanh u) with u = sqrt(2 / pi) (x + 0.044715 x^3). Since
+// 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)), it is evaluated as x / (1 + exp(-2 u)), which does not cancel.
+constexpr float kGeluTanhC0 = 1.5957691216057307117f;                  // 2 sqrt(2 / pi)
+constexpr float kGeluTanhC1 = 1.5957691216057307117f * 0.044715f;
+__device__ __forceinline__ float gelu_tanh_f32(float x) {
+  return __fdividef(x, 1.0f + expf(-x * fmaf(kGeluTanhC1, x * x, kGeluTanhC0)));
+}
+
+// act'(x) of every activation of the linear layers' epilogues. The logistic functions are formed from
+// t = exp(-|z|) <= 1, so neither side cancels or overflows: sigmoid = 1 / (1 + t) or t / (1 + t), and
+// sigmoid (1 - sigmoid) = t / (1 + t)^2. Beyond |x| = 20 the tanh form's derivative is exactly 0 or 1.
+__device__ __forceinline__ float act_grad_f32(float x, int act) {
+  if (act == kActGelu) return gelu_grad_f32(x);
+  if (act == kActRelu) return x > 0.0f ? 1.0f : 0.0f;
+  const bool tanh_form = act == kActGeluTanh;
+  if (tanh_form && fabsf(x) > 20.0f) return x > 0.0f ? 1.0f : 0.0f;
+  const float z = tanh_form ? x * fmaf(kGeluTanhC1, x * x, kGeluTanhC0) : x;
+  const float dz = tanh_form ? fmaf(3.0f * kGeluTanhC1, x * x, kGeluTanhC0) : 1.0f;
+  const float t = expf(-fabsf(z)), r = __fdividef(1.0f, 1.0f + t);
+  return fmaf(x * dz, t * r * r, z >= 0.0f ? r : t * r);
 }
 
 }  // namespace jf

@@ -161,6 +161,7 @@ int gemm_call(int mode, const jf_cqtensor& A, const jf_cqtensor& B, const jf_qte
   g.act = act;
   g.pre_q = pre.q;
   g.pre_s = pre.q ? pre.s : nullptr;
+  g.ep = nullptr;
   g.status = d.status;
   if (depth == 0) {
     // empty contraction: the result is exactly zero (codes 0, scales 0)
@@ -532,6 +533,300 @@ int jf_mx_linear_fwd(const uint8_t* a_codes, const uint8_t* a_scales, const uint
                                         static_cast<cudaStream_t>(stream)));
 }
 
+namespace {
+
+bool dtype_ok(jf_dtype dt) { return dt == JF_F32 || dt == JF_BF16 || dt == JF_F16; }
+
+// A dense [rows, cols] operand of the epilogue calls, and the bytes from its first to its last element.
+int check_matrix(const void* p, jf_dtype dt, int64_t ld, int64_t cols) {
+  if (p == nullptr) return JF_OK;
+  if (!dtype_ok(dt)) return JF_ERR_DTYPE;
+  if (ld < cols || ld >= (int64_t(1) << 40)) return JF_ERR_SHAPE;
+  if (!aligned(p, 16) || (ld * elem_size(dt)) % 16 != 0) return JF_ERR_ALIGN;
+  return JF_OK;
+}
+int64_t extent(jf_dtype dt, int64_t ld, int64_t rows, int64_t cols) { return ((rows - 1) * ld + cols) * elem_size(dt); }
+
+// The linear layer's forward (bias, pre-activation output) and input gradient (saved pre-activation input)
+// with activation and residual. rows x cols: the output; depth: the contraction.
+int epilogue_call(int mode, const jf_cqtensor& A, const jf_cqtensor& B, const float* bias, const jf_cqtensor& saved,
+                  jf_activation act, const jf_cqtensor& Rq, const jf_cmatrix& R, const jf_qtensor& Y, const jf_matrix& y,
+                  const jf_qtensor& pre, int64_t rows, int64_t cols, int64_t depth, void* stream) {
+  int st;
+  if (act < JF_ACT_NONE || act > JF_ACT_SILU) return JF_ERR_ARG;
+  if ((st = check_cq(A)) != JF_OK) return st;
+  if ((st = check_cq(B)) != JF_OK) return st;
+  const bool want_saved = mode == jf::kDgrad && act != JF_ACT_NONE;
+  if (want_saved && ((st = check_cq(saved)) != JF_OK)) return st;
+  if (want_saved && (saved.rows != rows || saved.cols != cols)) return JF_ERR_SHAPE;
+  if (Rq.q != nullptr && R.p != nullptr) return JF_ERR_ARG;
+  if (Rq.q != nullptr) {
+    if ((st = check_cq(Rq)) != JF_OK) return st;
+    if (Rq.rows != rows || Rq.cols != cols) return JF_ERR_SHAPE;
+  }
+  if ((st = check_matrix(R.p, R.dt, R.ld, cols)) != JF_OK) return st;
+  if ((st = check_matrix(y.p, y.dt, y.ld, cols)) != JF_OK) return st;
+  const jf_qtensor* const outs_q[2] = {&Y, &pre};
+  for (const jf_qtensor* o : outs_q) {
+    if (o->q == nullptr) continue;
+    if ((st = check_q(*o, true)) != JF_OK) return st;
+    if (o->rows != rows || o->cols != cols) return JF_ERR_SHAPE;
+  }
+  if (rows == 0 || cols == 0) return JF_OK;
+  if (Y.q == nullptr && y.p == nullptr) return JF_ERR_NULL;
+  if (!aligned(bias, 16)) return JF_ERR_ALIGN;
+  const int64_t nq = rows * cols, ns = sbytes(rows, cols);
+  const int64_t ny = y.p ? extent(y.dt, y.ld, rows, cols) : 0, nr = R.p ? extent(R.dt, R.ld, rows, cols) : 0;
+  const bool in_place = y.p != nullptr && y.p == R.p && y.dt == R.dt && y.ld == R.ld;
+  const void* ins[10] = {A.q, A.s, B.q, B.s, bias, want_saved ? saved.q : nullptr, want_saved ? saved.s : nullptr, Rq.q,
+                         Rq.q ? Rq.s : nullptr, R.p};
+  const int64_t in_n[10] = {qbytes(A), sbytes(A.rows, A.cols), qbytes(B), sbytes(B.rows, B.cols), cols * 4, nq, ns, nq, ns, nr};
+  const void* outs[5] = {Y.q, Y.q ? Y.s : nullptr, y.p, pre.q, pre.q ? pre.s : nullptr};
+  const int64_t out_n[5] = {nq, ns, ny, nq, ns};
+  for (int o = 0; o < 5; ++o) {
+    for (int i = 0; i < 10; ++i)
+      if (overlap(outs[o], out_n[o], ins[i], in_n[i]) && !(o == 2 && i == 9 && in_place)) return JF_ERR_ALIAS;
+    for (int o2 = o + 1; o2 < 5; ++o2)
+      if (overlap(outs[o], out_n[o], outs[o2], out_n[o2])) return JF_ERR_ALIAS;
+  }
+  const DevInfo d = device_info();
+  if (!d.ok) return JF_ERR_DEVICE;
+  jf::GemmEpilogue e = {};
+  e.bias = bias;
+  if (want_saved) {
+    e.act_q = saved.q;
+    e.act_s = saved.s;
+  }
+  if (Rq.q != nullptr) {
+    e.res = Rq.q;
+    e.res_s = Rq.s;
+    e.res_type = jf::kResI8;
+  } else if (R.p != nullptr) {
+    e.res = R.p;
+    e.res_type = int(R.dt);
+    e.res_ld = R.ld;
+  }
+  e.y = y.p;
+  e.y_type = y.p ? int(y.dt) : 0;
+  e.y_ld = y.ld;
+  jf::GemmArgs g = {};
+  g.mode = mode;
+  g.a_q = A.q;
+  g.a_s = A.s;
+  g.b_q = B.q;
+  g.b_s = B.s;
+  g.rows = rows;
+  g.cols = cols;
+  g.depth = depth;
+  g.a_ld = A.cols;
+  g.b_ld = B.cols;
+  g.y_q = Y.q;
+  g.y_s = Y.q ? Y.s : nullptr;
+  g.act = int(act);
+  g.pre_q = pre.q;
+  g.pre_s = pre.q ? pre.s : nullptr;
+  g.ep = &e;
+  g.status = d.status;
+  return cuda_status(jf::launch_gemm(g, d.sm_count, static_cast<cudaStream_t>(stream)));
+}
+
+// The description shared by the two QKV calls.
+int check_qkv(int64_t rows, const jf_qkv_rope* a) {
+  if (a == nullptr) return JF_ERR_NULL;
+  const int64_t lim = int64_t(1) << 31;
+  if (a->layout != JF_ROPE_HALF && a->layout != JF_ROPE_INTERLEAVED) return JF_ERR_ARG;
+  if (!(a->eps > 0.0f)) return JF_ERR_ARG;
+  if (a->batch < 0 || a->seq < 0 || a->batch >= lim || a->seq >= lim || a->q_heads < 0 || a->kv_heads < 0 ||
+      a->q_heads > 65535 || a->kv_heads > 65535 || a->head_dim < 32 || a->head_dim > 256 || a->head_dim % 32 != 0 ||
+      a->rot_dim < 0 || a->rot_dim > a->head_dim || a->rot_dim % 16 != 0 || a->table_len < 0 || a->table_len >= lim * lim / 512 ||
+      a->batch * a->seq > rows)
+    return JF_ERR_SHAPE;
+  if (a->rot_dim > 0 && a->positions == nullptr && a->seq > a->table_len) return JF_ERR_SHAPE;
+  return JF_OK;
+}
+
+// One dense tensor of heads; bytes: from the first to the last element.
+int check_heads(const void* p, const int64_t (&stride)[3], const int64_t (&size)[3], int64_t d, int64_t es, bool output,
+                int64_t& bytes) {
+  bytes = 0;
+  if (size[0] == 0 || size[1] == 0 || size[2] == 0) return JF_OK;
+  if (p == nullptr) return JF_ERR_NULL;
+  if (!aligned(p, 16)) return JF_ERR_ALIGN;
+  int64_t last = d - 1;
+  for (int k = 0; k < 3; ++k) {
+    if (size[k] == 1) continue;
+    if (stride[k] < 0 || stride[k] >= (int64_t(1) << 40)) return JF_ERR_SHAPE;
+    if ((stride[k] * es) % 16 != 0) return JF_ERR_ALIGN;
+    last += stride[k] * (size[k] - 1);
+  }
+  if (output) {   // from the smallest stride up, each must step over all that lies below it
+    int64_t below = d;
+    bool done[3] = {size[0] == 1, size[1] == 1, size[2] == 1};
+    for (int n = 0; n < 3; ++n) {
+      int best = -1;
+      for (int k = 0; k < 3; ++k)
+        if (!done[k] && (best < 0 || stride[k] < stride[best])) best = k;
+      if (best < 0) break;
+      if (stride[best] < below) return JF_ERR_SHAPE;
+      below = stride[best] * (size[best] - 1) + below;
+      done[best] = true;
+    }
+  }
+  bytes = (last + 1) * es;
+  return JF_OK;
+}
+
+int qkv_call(bool backward, const jf_cqtensor& X, const jf_qkv_rope* a, const jf_cheads (&t)[3], jf_dtype dt,
+             const jf_qtensor& dX, float* dgq, float* dgk, void* workspace, int64_t workspace_bytes, void* stream) {
+  int st;
+  if (!dtype_ok(dt)) return JF_ERR_DTYPE;
+  if (!dims_ok(X.rows, X.cols)) return JF_ERR_SHAPE;
+  if ((st = check_qkv(X.rows, a)) != JF_OK) return st;
+  if (X.cols != (a->q_heads + 2 * a->kv_heads) * a->head_dim) return JF_ERR_SHAPE;
+  if (backward && (dX.rows != X.rows || dX.cols != X.cols)) return JF_ERR_SHAPE;
+  const int64_t tokens = a->batch * a->seq, d = a->head_dim;
+  const bool norm = (a->gamma_q != nullptr && a->q_heads > 0) || (a->gamma_k != nullptr && a->kv_heads > 0);
+  const bool rotates = a->rot_dim > 0 && tokens > 0 && X.cols > 0;
+  if ((dgq != nullptr && a->gamma_q == nullptr) || (dgk != nullptr && a->gamma_k == nullptr)) return JF_ERR_NULL;
+  const bool want_dg = dgq != nullptr || dgk != nullptr;
+  const bool reads_x = (!backward || norm) && tokens > 0;
+  if (reads_x && (st = check_cq(X)) != JF_OK) return st;
+  if (backward && (st = check_q(dX, true)) != JF_OK) return st;
+  if (rotates && (a->cos_table == nullptr || a->sin_table == nullptr)) return JF_ERR_NULL;
+  if (!aligned(a->cos_table, 16) || !aligned(a->sin_table, 16) || !aligned(a->positions, 8) || !aligned(a->gamma_q, 16) ||
+      !aligned(a->gamma_k, 16) || !aligned(dgq, 4) || !aligned(dgk, 4))
+    return JF_ERR_ALIGN;
+  int64_t tb[3];
+  for (int k = 0; k < 3; ++k) {
+    const int64_t stride[3] = {t[k].stride_b, t[k].stride_s, t[k].stride_h};
+    const int64_t size[3] = {a->batch, a->seq, k == 0 ? a->q_heads : a->kv_heads};
+    if ((st = check_heads(t[k].p, stride, size, d, elem_size(dt), !backward, tb[k])) != JF_OK) return st;
+  }
+  const int64_t nq = X.rows * X.cols, ns = sbytes(X.rows, X.cols);
+  const int64_t ntab = rotates ? a->table_len * (a->rot_dim / 2) * 4 : 0;
+  const void* ins[10] = {reads_x ? X.q : nullptr, reads_x ? X.s : nullptr, a->cos_table, a->sin_table, a->positions,
+                         a->gamma_q, a->gamma_k, backward ? t[0].p : nullptr, backward ? t[1].p : nullptr,
+                         backward ? t[2].p : nullptr};
+  const int64_t in_n[10] = {nq, ns, ntab, ntab, rotates ? tokens * 8 : 0, d * 4, d * 4, tb[0], tb[1], tb[2]};
+  const int64_t nw = want_dg ? jf::qkv_bwd_ctas(X.rows, a->q_heads, a->kv_heads) * 2 * d * 4 : 0;
+  if (want_dg && (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < nw)) return JF_ERR_WORKSPACE;
+  const void* fo[3] = {t[0].p, t[1].p, t[2].p};
+  const void* bo[5] = {dX.q, dX.s, dgq, dgk, want_dg ? workspace : nullptr};
+  const int64_t bo_n[5] = {nq, ns, d * 4, d * 4, nw};
+  for (int i = 0; i < 10; ++i) {
+    if (!backward)
+      for (int o = 0; o < 3; ++o)
+        if (overlap(fo[o], tb[o], ins[i], in_n[i])) return JF_ERR_ALIAS;
+    if (backward)
+      for (int o = 0; o < 5; ++o)
+        if (overlap(bo[o], bo_n[o], ins[i], in_n[i])) return JF_ERR_ALIAS;
+  }
+  if (backward)
+    for (int o = 0; o < 5; ++o)
+      for (int o2 = o + 1; o2 < 5; ++o2)
+        if (overlap(bo[o], bo_n[o], bo[o2], bo_n[o2])) return JF_ERR_ALIAS;
+  if (!backward && (tokens == 0 || X.cols == 0)) return JF_OK;
+  if (backward && nq == 0 && !want_dg) return JF_OK;
+  const DevInfo dev = device_info();
+  if (!dev.ok) return JF_ERR_DEVICE;
+  jf::QkvRopeArgs g = {};
+  g.x_q = X.q;
+  g.x_s = X.s;
+  g.rows = X.rows;
+  g.cols = X.cols;
+  g.tokens = tokens;
+  g.seq = a->seq > 0 ? a->seq : 1;
+  g.hq = int(a->q_heads);
+  g.hkv = int(a->kv_heads);
+  g.d = int(d);
+  g.rot = int(a->rot_dim);
+  g.interleaved = a->layout == JF_ROPE_INTERLEAVED;
+  g.cos = a->cos_table;
+  g.sin = a->sin_table;
+  g.table_len = a->table_len;
+  g.positions = a->positions;
+  g.gamma_q = a->gamma_q;
+  g.gamma_k = a->gamma_k;
+  g.eps = a->eps;
+  jf::DenseHeads* const h[3] = {&g.q, &g.k, &g.v};
+  for (int k = 0; k < 3; ++k) *h[k] = jf::DenseHeads{const_cast<void*>(t[k].p), t[k].stride_b, t[k].stride_s, t[k].stride_h};
+  g.dx_q = dX.q;
+  g.dx_s = dX.s;
+  g.part = want_dg ? static_cast<float*>(workspace) : nullptr;
+  g.dgamma_q = dgq;
+  g.dgamma_k = dgk;
+  g.status = dev.status;
+  return cuda_status(jf::launch_qkv_rope(g, backward, int(dt), dev.sm_count, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+int jf_linear_fwd_epilogue(jf_cqtensor X, jf_cqtensor W, const float* bias, jf_activation act, jf_cqtensor Rq,
+                           jf_cmatrix R, jf_qtensor Y, jf_matrix y, jf_qtensor P, void* stream) {
+  JF_RANGE(__func__);
+  if (!dims_ok(X.rows, X.cols) || !dims_ok(W.rows, W.cols)) return JF_ERR_SHAPE;
+  if (X.cols != W.cols) return JF_ERR_SHAPE;
+  return epilogue_call(jf::kFwd, X, W, bias, jf_cqtensor{nullptr, nullptr, 0, 0}, act, Rq, R, Y, y, P, X.rows, W.rows,
+                       X.cols, stream);
+}
+
+int jf_linear_dgrad_epilogue(jf_cqtensor dY, jf_cqtensor W, jf_cqtensor P, jf_activation act, jf_cqtensor Rq,
+                             jf_cmatrix R, jf_qtensor Y, jf_matrix y, void* stream) {
+  JF_RANGE(__func__);
+  if (!dims_ok(dY.rows, dY.cols) || !dims_ok(W.rows, W.cols)) return JF_ERR_SHAPE;
+  if (dY.cols != W.rows) return JF_ERR_SHAPE;
+  return epilogue_call(jf::kDgrad, dY, W, nullptr, P, act, Rq, R, Y, y, jf_qtensor{nullptr, nullptr, 0, 0}, dY.rows, W.cols,
+                       dY.cols, stream);
+}
+
+int jf_bias_grad(jf_cqtensor dY, float* db, void* stream) {
+  JF_RANGE(__func__);
+  int st;
+  if ((st = check_cq(dY)) != JF_OK) return st;
+  if (dY.cols == 0) return JF_OK;
+  if (db == nullptr) return JF_ERR_NULL;
+  if (!aligned(db, 4)) return JF_ERR_ALIGN;
+  if (dY.rows != 0 && (overlap(db, dY.cols * 4, dY.q, qbytes(dY)) || overlap(db, dY.cols * 4, dY.s, sbytes(dY.rows, dY.cols))))
+    return JF_ERR_ALIAS;
+  const DevInfo d = device_info();
+  if (!d.ok) return JF_ERR_DEVICE;
+  return cuda_status(jf::launch_bias_grad(dY.q, dY.s, dY.rows, dY.cols, db, static_cast<cudaStream_t>(stream)));
+}
+
+int jf_rope_table(const double* inv_freq, int64_t half, double magnitude, int64_t length, float* cos_table, float* sin_table,
+                  void* stream) {
+  JF_RANGE(__func__);
+  if (half < 1 || half > 128 || length < 0 || length >= (int64_t(1) << 40)) return JF_ERR_SHAPE;
+  if (length == 0) return JF_OK;
+  if (inv_freq == nullptr || cos_table == nullptr || sin_table == nullptr) return JF_ERR_NULL;
+  if (!aligned(cos_table, 16) || !aligned(sin_table, 16)) return JF_ERR_ALIGN;
+  if (overlap(cos_table, length * half * 4, sin_table, length * half * 4)) return JF_ERR_ALIAS;
+  const DevInfo d = device_info();
+  if (!d.ok) return JF_ERR_DEVICE;
+  return cuda_status(jf::launch_rope_table(inv_freq, half, magnitude, length, cos_table, sin_table, d.sm_count,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+int64_t jf_qkv_rope_bwd_workspace_bytes(int64_t rows, const jf_qkv_rope* a) {
+  if (rows < 0 || rows % 32 != 0 || rows >= (int64_t(1) << 31) || check_qkv(rows, a) != JF_OK) return -1;
+  return jf::qkv_bwd_ctas(rows, a->q_heads, a->kv_heads) * 2 * a->head_dim * 4;
+}
+
+int jf_qkv_rope_fwd(jf_cqtensor QKV, const jf_qkv_rope* a, jf_heads q, jf_heads k, jf_heads v, jf_dtype dt, void* stream) {
+  JF_RANGE(__func__);
+  const jf_cheads t[3] = {{q.p, q.stride_b, q.stride_s, q.stride_h}, {k.p, k.stride_b, k.stride_s, k.stride_h},
+                          {v.p, v.stride_b, v.stride_s, v.stride_h}};
+  return qkv_call(false, QKV, a, t, dt, jf_qtensor{nullptr, nullptr, 0, 0}, nullptr, nullptr, nullptr, 0, stream);
+}
+
+int jf_qkv_rope_bwd(jf_cqtensor QKV, const jf_qkv_rope* a, jf_cheads dq, jf_cheads dk, jf_cheads dv, jf_dtype dt,
+                    jf_qtensor dQKV, float* dgamma_q, float* dgamma_k, void* workspace, int64_t workspace_bytes,
+                    void* stream) {
+  JF_RANGE(__func__);
+  const jf_cheads t[3] = {dq, dk, dv};
+  return qkv_call(true, QKV, a, t, dt, dQKV, dgamma_q, dgamma_k, workspace, workspace_bytes, stream);
+}
+
 int jf_gemm_i8_s32(const int8_t* A, const int8_t* B, int32_t* C, int64_t M, int64_t N, int64_t K, void* stream) {
   JF_RANGE(__func__);
   if (M < 0 || N < 0 || K < 0 || M % 128 != 0 || N % 256 != 0 || K % 128 != 0 || K > 65536 ||
@@ -570,7 +865,8 @@ const char* jf_strerror(int status) {
     case JF_ERR_TIMEOUT: return "a kernel's bounded wait timed out; outputs are undefined";
     case JF_ERR_DEVICE: return "no usable sm_100 (B200) device is current";
     case JF_ERR_WORKSPACE: return "workspace is NULL, not 16-byte aligned or smaller than the size asked for";
-    case JF_ERR_ARG: return "unknown granularity (or other enumerated argument)";
+    case JF_ERR_ARG: return "an enumerated argument (granularity, activation, layout) is unknown, or a scalar one out of range";
+    case JF_ERR_RANGE: return "a position lay outside the rotary table; its token's rotated part is undefined";
     default: return "unknown status";
   }
 }
@@ -582,6 +878,7 @@ int jf_device_status(void* stream) {
   if (cudaMemcpyFromSymbol(&v, jf::g_status, sizeof(v)) != cudaSuccess) return JF_ERR_CUDA;
   if (v != 0 && cudaMemcpyToSymbol(jf::g_status, &zero, sizeof(zero)) != cudaSuccess) return JF_ERR_CUDA;
   if (v & jf::kStatusTimeout) return JF_ERR_TIMEOUT;
+  if (v & jf::kStatusRange) return JF_ERR_RANGE;
   return v ? JF_ERR_CUDA : JF_OK;
 }
 

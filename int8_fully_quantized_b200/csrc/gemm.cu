@@ -60,6 +60,7 @@
 #include <cuda_runtime.h>
 
 #include "act.cuh"
+#include "epilogue.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 #include "quant.cuh"
@@ -87,7 +88,11 @@ constexpr int SMEM_B = SMEM_A + STAGES * A_STAGE;
 constexpr int SMEM_BAR = SMEM_B + STAGES * B_STAGE;
 constexpr int NUM_BARS = 2 * STAGES + NBUF + NUM_MMA_WARPS;
 constexpr int SMEM_MISC = SMEM_BAR + NUM_BARS * 8;
-constexpr int SMEM_BYTES = SMEM_MISC + 16 + 1024;  // + slack to align the base to 1024
+constexpr int SMEM_STAGE = (SMEM_MISC + 16 + 127) / 128 * 128;   // the epilogue warps' staging areas
+constexpr int SMEM_BYTES = SMEM_STAGE + NUM_EPI_WARPS * kStageBytes + 1024;  // + slack to align the base to 1024
+// What a tile's epilogue does: the plain products, or a linear layer's forward / input gradient with
+// bias, activation and residual.
+enum Epilogue { kEpiPlain = 0, kEpiForward = 1, kEpiGrad = 2 };
 
 struct __align__(64) GemmParams {
   CUtensorMap tma_a;
@@ -107,6 +112,7 @@ struct __align__(64) GemmParams {
   int rows, cols, kblocks;
   int tiles_m, tiles_n;
   int n_fast;   // tile order: 0 = row tiles vary fastest, 1 = column tiles vary fastest
+  EpilogueParams ep;   // kEpiForward / kEpiGrad only
 };
 
 // Row and column tile of the CTA's tile t. The 148 tiles in flight at once share one operand's
@@ -154,7 +160,7 @@ __device__ __forceinline__ float scale_window(const float* __restrict__ base, in
   return (blk < nblk && kb < kblocks) ? __ldg(base + blk * s_blk + int64_t(kb) * s_k) : 0.0f;
 }
 
-template <bool A_MN, bool B_MN>
+template <bool A_MN, bool B_MN, int EPI>
 __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_i8_kernel(const __grid_constant__ GemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -180,8 +186,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_i8_kernel(const __grid_co
   }
   if (warp == 0) {
     if (lane == 0) {
-      prefetch_tensormap(&p.tma_a);
-      prefetch_tensormap(&p.tma_b);
+      if (p.kblocks > 0) {   // an empty contraction has no operands and no maps
+        prefetch_tensormap(&p.tma_a);
+        prefetch_tensormap(&p.tma_b);
+      }
     }
     __syncwarp();
     tmem_alloc(tmem_holder, TMEM_COLS);
@@ -362,26 +370,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_i8_kernel(const __grid_co
         }
       }
 
-      // ---- on-chip re-quantization of this warp's two 32x32 blocks of the finished tile (the loop is
-      // unrolled so that acc stays in registers)
+      if constexpr (EPI != kEpiPlain) {
+        if (rbk < nrb && cbk < ncb)
+          linear_epilogue<EPI == kEpiGrad>(p.ep, p.act, acc, p.y_q, p.y_s, p.pre_q, p.pre_s, p.ld_y, rbk, cbk, ncb,
+                                           cbk + 1 < ncb, smem + SMEM_STAGE + (warp - FIRST_EPI_WARP) * kStageBytes, lane);
+      } else {
+        // ---- on-chip re-quantization of this warp's two 32x32 blocks of the finished tile (the loop is
+        // unrolled so that acc stays in registers)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (rbk >= nrb || cbk + h >= ncb) continue;
-        float (&y)[32] = acc[h];
-        const int64_t off = (int64_t(rbk) * 32 + lane) * p.ld_y + int64_t(cbk + h) * 32;
-        const int64_t soff = int64_t(rbk) * ncb + cbk + h;
-        if (p.act == kActGelu) {
-          // fused activation: the fp32 pre-activation is re-quantized (when asked for) and GELU is
-          // applied to it on chip, so neither ever makes an HBM round trip in fp32
-          if (p.pre_q != nullptr) store_block_q(y, p.pre_q + off, p.pre_s + soff, lane);
+        for (int h = 0; h < 2; ++h) {
+          if (rbk >= nrb || cbk + h >= ncb) continue;
+          float (&y)[32] = acc[h];
+          const int64_t off = (int64_t(rbk) * 32 + lane) * p.ld_y + int64_t(cbk + h) * 32;
+          const int64_t soff = int64_t(rbk) * ncb + cbk + h;
+          if (p.act == kActGelu) {
+            // fused activation: the fp32 pre-activation is re-quantized (when asked for) and GELU is
+            // applied to it on chip, so neither ever makes an HBM round trip in fp32
+            if (p.pre_q != nullptr) store_block_q(y, p.pre_q + off, p.pre_s + soff, lane);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = gelu_f32(y[i]);
-        }
-        if (p.y_q != nullptr) store_block_q(y, p.y_q + off, p.y_s + soff, lane);
-        if (p.y_f32 != nullptr) {
-          float4* dst = reinterpret_cast<float4*>(p.y_f32 + off);
+            for (int i = 0; i < 32; ++i) y[i] = gelu_f32(y[i]);
+          }
+          if (p.y_q != nullptr) store_block_q(y, p.y_q + off, p.y_s + soff, lane);
+          if (p.y_f32 != nullptr) {
+            float4* dst = reinterpret_cast<float4*>(p.y_f32 + off);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          }
         }
       }
     }
@@ -568,10 +582,10 @@ static bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool A_MN, bool B_MN>
+template <bool A_MN, bool B_MN, int EPI>
 static cudaError_t run(const GemmParams& prm, int grid, cudaStream_t st) {
   static unsigned long long attr_set = 0;  // one bit per device ordinal
-  auto kern = gemm_i8_kernel<A_MN, B_MN>;
+  auto kern = gemm_i8_kernel<A_MN, B_MN, EPI>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -590,25 +604,26 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t st) {
   memset(&prm, 0, sizeof(prm));
   const int64_t rb = g.rows / 32, cb = g.cols / 32, kbn = g.depth / 32;
   bool a_mn = false, b_mn = false;
-  bool okA, okB;
+  bool okA = true, okB = true;
+  const bool operands = g.depth > 0;   // without a contraction (bias and residual alone) nothing is loaded
   switch (g.mode) {
     case kFwd:  // A = X [rows, depth], B = W [cols, depth]; both K-major
-      okA = make_map(&prm.tma_a, g.a_q, g.depth, g.rows, g.a_ld, 128, BM);
-      okB = make_map(&prm.tma_b, g.b_q, g.depth, g.cols, g.b_ld, 128, BN);
+      okA = !operands || make_map(&prm.tma_a, g.a_q, g.depth, g.rows, g.a_ld, 128, BM);
+      okB = !operands || make_map(&prm.tma_b, g.b_q, g.depth, g.cols, g.b_ld, 128, BN);
       prm.a_s_blk = kbn; prm.a_s_k = 1;
       prm.b_s_blk = kbn; prm.b_s_k = 1;
       break;
     case kDgrad:  // A = dY [rows, depth] K-major; B = W [depth, cols] MN-major
       b_mn = true;
-      okA = make_map(&prm.tma_a, g.a_q, g.depth, g.rows, g.a_ld, 128, BM);
-      okB = make_map(&prm.tma_b, g.b_q, g.cols, g.depth, g.b_ld, 128, 128);
+      okA = !operands || make_map(&prm.tma_a, g.a_q, g.depth, g.rows, g.a_ld, 128, BM);
+      okB = !operands || make_map(&prm.tma_b, g.b_q, g.cols, g.depth, g.b_ld, 128, 128);
       prm.a_s_blk = kbn; prm.a_s_k = 1;
       prm.b_s_blk = 1; prm.b_s_k = cb;
       break;
     default:  // kWgrad: A = dY [depth, rows] MN-major; B = X [depth, cols] MN-major
       a_mn = b_mn = true;
-      okA = make_map(&prm.tma_a, g.a_q, g.rows, g.depth, g.a_ld, 128, 128);
-      okB = make_map(&prm.tma_b, g.b_q, g.cols, g.depth, g.b_ld, 128, 128);
+      okA = !operands || make_map(&prm.tma_a, g.a_q, g.rows, g.depth, g.a_ld, 128, 128);
+      okB = !operands || make_map(&prm.tma_b, g.b_q, g.cols, g.depth, g.b_ld, 128, 128);
       prm.a_s_blk = 1; prm.a_s_k = rb;
       prm.b_s_blk = 1; prm.b_s_k = cb;
       break;
@@ -632,9 +647,24 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t st) {
   prm.tiles_n = int((g.cols + BN - 1) / BN);
   const int tiles = prm.tiles_m * prm.tiles_n;
   const int grid = tiles < sm_count ? tiles : sm_count;
-  if (!a_mn && !b_mn) return run<false, false>(prm, grid, st);
-  if (!a_mn && b_mn) return run<false, true>(prm, grid, st);
-  return run<true, true>(prm, grid, st);
+  if (g.ep != nullptr) {
+    const auto bytes = [](int type) { return int64_t(type == kDenseF32 ? 4 : 2); };
+    const GemmEpilogue& e = *g.ep;
+    prm.ep.bias = e.bias;
+    prm.ep.act_q = e.act_q;
+    prm.ep.act_s = e.act_s;
+    prm.ep.res = static_cast<const uint8_t*>(e.res);
+    prm.ep.res_s = e.res_s;
+    prm.ep.res_type = e.res_type;
+    prm.ep.res_ld = e.res_ld * bytes(e.res_type);
+    prm.ep.y = static_cast<uint8_t*>(e.y);
+    prm.ep.y_type = e.y_type;
+    prm.ep.y_ld = e.y_ld * bytes(e.y_type);
+    return b_mn ? run<false, true, kEpiGrad>(prm, grid, st) : run<false, false, kEpiForward>(prm, grid, st);
+  }
+  if (!a_mn && !b_mn) return run<false, false, kEpiPlain>(prm, grid, st);
+  if (!a_mn && b_mn) return run<false, true, kEpiPlain>(prm, grid, st);
+  return run<true, true, kEpiPlain>(prm, grid, st);
 }
 
 cudaError_t launch_gemm_s32(const int8_t* a, const int8_t* b, int32_t* c, int64_t M, int64_t N, int64_t K,

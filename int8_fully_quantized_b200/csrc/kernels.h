@@ -58,11 +58,64 @@ cudaError_t launch_layernorm_i8(const int8_t* q, const float* s, int64_t R, int6
                                 const float* beta, float eps, int8_t* qo, float* so, const int32_t* stats,
                                 cudaStream_t st);
 
+// Column sums of an INT8 tensor (bias_grad.cu).
+cudaError_t launch_bias_grad(const int8_t* q, const float* s, int64_t R, int64_t C, float* db, cudaStream_t st);
+
+// Per-head norm and rotary positions between the INT8 QKV tensor and dense heads (qkv_rope.cu).
+struct DenseHeads {           // element (batch b, token t, head h, dimension 0) at p + b stride_b + t stride_t + h stride_h
+  void* p;
+  int64_t stride_b, stride_t, stride_h;
+};
+struct QkvRopeArgs {
+  const int8_t* x_q;          // [rows, cols] codes and scales of the projection's output
+  const float* x_s;
+  int64_t rows, cols;
+  int64_t tokens, seq;        // valid rows; tokens of a sequence (row = batch * seq + token)
+  int hq, hkv, d, rot;
+  bool interleaved;
+  const float* cos;           // [table_len, rot / 2]
+  const float* sin;
+  int64_t table_len;
+  const int64_t* positions;   // [tokens], null: the token's index in its sequence
+  const float* gamma_q;       // [d] norm weights, null: no norm
+  const float* gamma_k;
+  float eps;
+  DenseHeads q, k, v;         // forward: outputs; backward: the gradients dq, dk, dv
+  int8_t* dx_q;               // backward outputs
+  float* dx_s;
+  float* part;                // backward workspace [ctas][2][d], null when no weight gradient is wanted
+  float* dgamma_q;
+  float* dgamma_k;
+  unsigned int* status;
+};
+int64_t qkv_bwd_ctas(int64_t rows, int64_t hq, int64_t hkv);
+cudaError_t launch_qkv_rope(const QkvRopeArgs& a, bool backward, int dtype, int sm_count, cudaStream_t st);
+// Tables of cos and sin (position * inv_freq[j]) * magnitude, [length, half], half <= 128; inv_freq is host memory.
+cudaError_t launch_rope_table(const double* inv_freq, int64_t half, double magnitude, int64_t length, float* cos_out,
+                              float* sin_out, int sm_count, cudaStream_t st);
+
 // Block-scaled INT8 GEMM: out[r, c] = sum over 32-blocks kb of the contraction axis of
 // fp32(sA(r/32, kb) * sB(c/32, kb)) * sum_{k in kb} A(r, k) B(c, k), re-quantized per 32x32 block.
 // The operand views differ per mode (see gemm.cu).
 enum GemmMode { kFwd = 0, kDgrad = 1, kWgrad = 2 };
-enum GemmAct { kActNone = 0, kActGelu = 1 };
+enum GemmAct { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+// Element type of a dense matrix (jf_dtype's values) or an INT8 residual.
+enum DenseType { kDenseF32 = 0, kDenseBf16 = 1, kDenseF16 = 2, kResI8 = 3 };
+
+// The parts of a linear layer's epilogue beyond the product (see epilogue.cuh): what the forward and the
+// input-gradient calls with bias / activation / residual add to GemmArgs. Null pointers are absent parts.
+struct GemmEpilogue {
+  const float* bias;          // forward: fp32 [cols]
+  const int8_t* act_q;        // input gradient: the saved pre-activation
+  const float* act_s;
+  const void* res;            // residual; res_type a DenseType, res_s the scales of an INT8 one
+  const float* res_s;
+  int res_type;
+  int64_t res_ld;             // row pitch of a dense residual, elements
+  void* y;                    // dense output
+  int y_type;
+  int64_t y_ld;
+};
 
 struct GemmArgs {
   int mode;
@@ -76,8 +129,9 @@ struct GemmArgs {
   float* y_s;                 // non-null when y_q is
   float* y_f32;               // nullable
   int act;                    // GemmAct: activation applied to the fp32 result before y is written
-  int8_t* pre_q;              // nullable (kActGelu only): the re-quantized pre-activation
+  int8_t* pre_q;              // nullable (an activated or biased forward only): the re-quantized pre-activation
   float* pre_s;               // non-null when pre_q is
+  const GemmEpilogue* ep;     // null: the plain epilogue (act kActNone or kActGelu)
   unsigned int* status;       // device status word (bit flags of ptx.cuh)
 };
 

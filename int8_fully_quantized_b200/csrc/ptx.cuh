@@ -7,8 +7,9 @@
 
 namespace jf {
 
-// Bit of the library's device status word (read and cleared by jf_device_status).
+// Bits of the library's device status word (read and cleared by jf_device_status).
 constexpr unsigned int kStatusTimeout = 1u;   // a bounded wait ran out
+constexpr unsigned int kStatusRange = 2u;     // a position outside the rotary table
 
 // A bounded wait gives up after this many nanoseconds of %globaltimer.
 constexpr unsigned long long kWatchdogNs = 4000000000ull;
