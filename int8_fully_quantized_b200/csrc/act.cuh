@@ -74,29 +74,77 @@ __device__ __forceinline__ void gelu_f32_x2(float& x0, float& x1) {
   x1 = 0.5f * x1 * (x1 >= 0.0f ? 2.0f - e1 : e1);
 }
 
-// SiLU(x) = x / (1 + exp(-x)). exp overflows to infinity for very negative x, where the quotient is 0.
-__device__ __forceinline__ float silu_f32(float x) { return __fdividef(x, 1.0f + expf(-x)); }
+// The hardware's approximate reciprocal (1 ulp) and power of two (2 ulp; results below 2^-126 become 0).
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634074f;
+
+// GELU of two values for the linear layers' epilogues, where the activation competes for issue slots with
+// the product itself: erfc_nonneg's fit with the approximate reciprocal and power of two (14 instructions
+// a value against 22), GELU(x) = max(x, 0) - |x e / 2|. The exponent's rounding, |log2| 2^-24, bounds the
+// relative error of e: below 2^-18 for |x| < 9.
+__device__ __forceinline__ void gelu_epilogue_x2(float& x0, float& x1) {
+  constexpr float c[10] = {0.17087277f, -0.82215223f, 1.48851587f, -1.13520398f, 0.27886807f,
+                           -0.18628806f, 0.09678418f, 0.37409196f, 1.00002368f, -1.26551223f};
+  float z0, z1, t0, t1, p0 = c[0], p1 = c[0], h0, h1;
+  mul_x2(fabsf(x0), fabsf(x1), 0.70710678118654752440f, 0.70710678118654752440f, z0, z1);
+  fma_x2(z0, z1, 0.5f, 0.5f, 1.0f, 1.0f, t0, t1);
+  t0 = rcp_approx(t0);
+  t1 = rcp_approx(t1);
+#pragma unroll
+  for (int i = 1; i < 10; ++i) fma_x2(p0, p1, t0, t1, c[i], c[i], p0, p1);
+  fma_x2(-z0, -z1, z0, z1, p0, p1, p0, p1);
+  mul_x2(p0, p1, kLog2e, kLog2e, p0, p1);
+  mul_x2(x0, x1, 0.5f, 0.5f, h0, h1);
+  mul_x2(h0, h1, t0, t1, h0, h1);
+  mul_x2(h0, h1, exp2_approx(p0), exp2_approx(p1), h0, h1);
+  x0 = fmaxf(x0, 0.0f) - fabsf(h0);
+  x1 = fmaxf(x1, 0.0f) - fabsf(h1);
+}
+
+// SiLU(x) = x / (1 + exp(-x)). The power overflows to infinity for very negative x, where the quotient is 0.
+__device__ __forceinline__ float silu_f32(float x) { return x * rcp_approx(1.0f + exp2_approx(-kLog2e * x)); }
 
 // The tanh form of GELU, 0.5 x (1 + tanh u) with u = sqrt(2 / pi) (x + 0.044715 x^3). Since
 // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)), it is evaluated as x / (1 + exp(-2 u)), which does not cancel.
 constexpr float kGeluTanhC0 = 1.5957691216057307117f;                  // 2 sqrt(2 / pi)
 constexpr float kGeluTanhC1 = 1.5957691216057307117f * 0.044715f;
 __device__ __forceinline__ float gelu_tanh_f32(float x) {
-  return __fdividef(x, 1.0f + expf(-x * fmaf(kGeluTanhC1, x * x, kGeluTanhC0)));
+  return x * rcp_approx(1.0f + exp2_approx(-x * fmaf(kLog2e * kGeluTanhC1, x * x, kLog2e * kGeluTanhC0)));
 }
 
-// act'(x) of every activation of the linear layers' epilogues. The logistic functions are formed from
-// t = exp(-|z|) <= 1, so neither side cancels or overflows: sigmoid = 1 / (1 + t) or t / (1 + t), and
-// sigmoid (1 - sigmoid) = t / (1 + t)^2. Beyond |x| = 20 the tanh form's derivative is exactly 0 or 1.
-__device__ __forceinline__ float act_grad_f32(float x, int act) {
-  if (act == kActGelu) return gelu_grad_f32(x);
+// act'(x) for x >= 0 of every activation of the linear layers' epilogues, with the approximate functions.
+// GELU: Phi(x) + x phi(x) from erfc_nonneg's fit; the logistic ones from t = exp(-z) <= 1, sigmoid = 1 / (1 + t)
+// and sigmoid (1 - sigmoid) = t / (1 + t)^2. Beyond x = 20 the tanh form's derivative is 1.
+__device__ __forceinline__ float act_grad_pos_f32(float x, int act) {
   if (act == kActRelu) return x > 0.0f ? 1.0f : 0.0f;
-  const bool tanh_form = act == kActGeluTanh;
-  if (tanh_form && fabsf(x) > 20.0f) return x > 0.0f ? 1.0f : 0.0f;
-  const float z = tanh_form ? x * fmaf(kGeluTanhC1, x * x, kGeluTanhC0) : x;
-  const float dz = tanh_form ? fmaf(3.0f * kGeluTanhC1, x * x, kGeluTanhC0) : 1.0f;
-  const float t = expf(-fabsf(z)), r = __fdividef(1.0f, 1.0f + t);
-  return fmaf(x * dz, t * r * r, z >= 0.0f ? r : t * r);
+  if (act == kActGeluEpi) {
+    constexpr float c[10] = {0.17087277f, -0.82215223f, 1.48851587f, -1.13520398f, 0.27886807f,
+                             -0.18628806f, 0.09678418f, 0.37409196f, 1.00002368f, -1.26551223f};
+    const float z = x * 0.70710678118654752440f;
+    const float t = rcp_approx(fmaf(0.5f, z, 1.0f));
+    float p = c[0];
+#pragma unroll
+    for (int i = 1; i < 10; ++i) p = fmaf(p, t, c[i]);
+    const float e = t * exp2_approx(kLog2e * fmaf(-z, z, p));
+    return fmaf(x * 0.39894228040143267794f, exp2_approx(-kLog2e * z * z), fmaf(-0.5f, e, 1.0f));
+  }
+  float z = x, dz = 1.0f;
+  if (act == kActGeluTanh) {
+    x = fminf(x, 20.0f);
+    z = x * fmaf(kGeluTanhC1, x * x, kGeluTanhC0);
+    dz = fmaf(3.0f * kGeluTanhC1, x * x, kGeluTanhC0);
+  }
+  const float t = exp2_approx(-kLog2e * z), r = rcp_approx(1.0f + t);
+  return fmaf(x * dz, t * r * r, r);
 }
 
 }  // namespace jf

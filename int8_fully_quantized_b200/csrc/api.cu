@@ -144,7 +144,7 @@ int gemm_call(int mode, const jf_cqtensor& A, const jf_cqtensor& B, const jf_qte
   }
   const DevInfo d = device_info();
   if (!d.ok) return JF_ERR_DEVICE;
-  jf::GemmArgs g;
+  jf::GemmArgs g = {};
   g.mode = mode;
   g.a_q = A.q;
   g.a_s = A.s;
@@ -157,11 +157,12 @@ int gemm_call(int mode, const jf_cqtensor& A, const jf_cqtensor& B, const jf_qte
   g.b_ld = B.cols;
   g.y_q = Y.q;
   g.y_s = Y.q ? Y.s : nullptr;
-  g.y_f32 = y_f32;
+  g.y = y_f32;
+  g.y_type = jf::kDenseF32;
+  g.y_ld = cols;
   g.act = act;
   g.pre_q = pre.q;
   g.pre_s = pre.q ? pre.s : nullptr;
-  g.ep = nullptr;
   g.status = d.status;
   if (depth == 0) {
     // empty contraction: the result is exactly zero (codes 0, scales 0)
@@ -591,24 +592,6 @@ int epilogue_call(int mode, const jf_cqtensor& A, const jf_cqtensor& B, const fl
   }
   const DevInfo d = device_info();
   if (!d.ok) return JF_ERR_DEVICE;
-  jf::GemmEpilogue e = {};
-  e.bias = bias;
-  if (want_saved) {
-    e.act_q = saved.q;
-    e.act_s = saved.s;
-  }
-  if (Rq.q != nullptr) {
-    e.res = Rq.q;
-    e.res_s = Rq.s;
-    e.res_type = jf::kResI8;
-  } else if (R.p != nullptr) {
-    e.res = R.p;
-    e.res_type = int(R.dt);
-    e.res_ld = R.ld;
-  }
-  e.y = y.p;
-  e.y_type = y.p ? int(y.dt) : 0;
-  e.y_ld = y.ld;
   jf::GemmArgs g = {};
   g.mode = mode;
   g.a_q = A.q;
@@ -622,10 +605,26 @@ int epilogue_call(int mode, const jf_cqtensor& A, const jf_cqtensor& B, const fl
   g.b_ld = B.cols;
   g.y_q = Y.q;
   g.y_s = Y.q ? Y.s : nullptr;
+  g.y = y.p;
+  g.y_type = y.p ? int(y.dt) : 0;
+  g.y_ld = y.ld;
+  g.bias = bias;
   g.act = int(act);
+  if (want_saved) {
+    g.act_q = saved.q;
+    g.act_s = saved.s;
+  }
   g.pre_q = pre.q;
   g.pre_s = pre.q ? pre.s : nullptr;
-  g.ep = &e;
+  if (Rq.q != nullptr) {
+    g.res = Rq.q;
+    g.res_s = Rq.s;
+    g.res_type = jf::kResI8;
+  } else if (R.p != nullptr) {
+    g.res = R.p;
+    g.res_type = int(R.dt);
+    g.res_ld = R.ld;
+  }
   g.status = d.status;
   return cuda_status(jf::launch_gemm(g, d.sm_count, static_cast<cudaStream_t>(stream)));
 }

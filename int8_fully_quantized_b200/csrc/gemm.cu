@@ -9,49 +9,49 @@
 // and accumulated in fp32; after the last block the fp32 tile is re-quantized per 32x32 block.
 //
 // Design of the block-scaled kernel (one CTA per SM, persistent over 128 x 128 output tiles, in the
-// order that keeps the smaller operand resident in L2: see tile_of). The
-// rescale needs, per output element and contraction block, an int32 -> fp32 conversion and an FMA
-// on the CUDA cores, several times the tensor core's time for the same block, so the kernel is
-// built to keep the epilogue warps busy; the tensor core only has to stay ahead of them. Each
-// contraction block of a tile is one MMA into its own int32 TMEM accumulator; four such
-// accumulators (all 512 TMEM columns) rotate, so the MMAs run up to four blocks ahead:
+// order that keeps the smaller operand resident in L2: see TileWalk). The rescale needs, per output
+// element and contraction block, a conversion and an FMA on the CUDA cores, several times the tensor core's
+// time for the same block, so the kernel is built to keep the warps that sum busy. Each contraction
+// block of a tile is one MMA into its own int32 TMEM accumulator of 128 columns; the four accumulators
+// that fit in TMEM form two groups of two, filled and emptied in turn:
 //   warp 0       producer: lane 0 loads 128-byte-deep stages of A and B (TMA, 128-byte swizzle,
-//                no multicast) into a 6-stage shared-memory ring; a slot is refilled once the MMAs
+//                no multicast) into a 4-stage shared-memory ring; a slot is refilled once the MMAs
 //                that read it have completed (tcgen05.commit on the slot's `empty` barrier).
-//   warps 1-2    MMA: warp 1 + m issues the MMAs (M=128, N=128, K=32, one per contraction block)
-//                of pipeline stages m, m + 2, ..., each committed to its accumulator's `tfull`
-//                barrier. It reuses accumulator b as soon as all epilogue warps have read it:
-//                they each bar.arrive on a hand-off hardware barrier after their TMEM load and the
-//                MMA warp waits there with bar.sync. Two warps alternate stages because a lone
-//                thread issues at most about one MMA per ~220 cycles.
-//   warps 3-10   epilogue: warp w owns TMEM lanes 32 (w % 4) .. +31 and two 32-column blocks, i.e.
-//                two 32x32 output blocks of the tile. Per contraction block it waits (bar.sync)
-//                for the watcher's signal, loads its 64 int32 partials per thread (one tcgen05.ld),
-//                arrives on the hand-off barrier, and accumulates fp32(sA*sB) * P in registers.
-//                The block scales come from global memory straight into registers, 32 contraction
-//                blocks per load (lane l holds block w0 + l), one window ahead, and are broadcast
-//                by warp shuffles. After the last block the warp reduces each block's absmax and
-//                writes its 32x32 codes, the block scale and (optionally) the fp32 result.
-//   warp 11      completion watcher: lane 0 is the only thread that polls the `tfull` mbarriers;
-//                once block g's MMA has completed it releases the epilogue warps through hardware
-//                barrier 9 + g % 4. Measured on B200: with all 256 epilogue threads polling the
-//                mbarriers instead, the MMA issue and commit latencies grew several-fold and the
-//                kernel ran ~35% slower.
-// Twelve warps keep at most three on an SM sub-partition, so each thread may hold 64 accumulators
-// and 64 partials in registers.
+//   warp 1       MMA: lane 0 issues a group's MMAs (M=128, N=128, K=32: for each of its two contraction
+//                blocks, one at a tile's odd end, one that sets the accumulator to a constant and one that
+//                adds the block's product; see partial_x2) and commits them together to the group's
+//                `tfull` barrier, once the sum warps have emptied the group (`tempty`).
+//   warps 4-11   sum: warp w owns TMEM lanes 32 (w % 4) .. +31 and two 32-column blocks, i.e.
+//                two 32x32 output blocks of the tile. It waits for the group, loads each block's 64
+//                partials per thread (one tcgen05.ld), hands the group back after the last load, and
+//                accumulates fp32(sA*sB) * P in registers. The block scales come from global memory
+//                straight into registers, 32 contraction blocks per load (lane l holds block w0 + l), one
+//                window ahead, and are broadcast by warp shuffles. After the last block it leaves its two
+//                fp32 blocks in shared memory (`ofull` / `oempty`) and goes on with the next tile.
+//   warps 12-..  output: four or eight warps (Roles) take the finished blocks through the tile's epilogue
+//                (epilogue.cuh) while the next tile is summed.
+// What bounds it (B200, 1965 MHz). Per 128 x 128 tile and contraction block the sum warps of a
+// sub-partition need 256 cycles of FMA pipe (two packed FMAs for 2 elements); measured 445-470 at a
+// contraction of 16384 and 490 with 8 output warps. The rest is latency the two warps of a sub-partition do
+// not hide for each other (barrier wait, TMEM load 80 cycles) and the hand-off: an MMA's result is visible ~530
+// cycles after its issue, two MMAs' ~620, and each commit holds the tensor pipe for ~57 cycles besides
+// an MMA's 64, which is why two blocks share one commit (389 cycles per block in a reduced kernel with two
+// groups of two, 473 with four of one) and why every thread of a sum warp polls the barrier itself (one
+// polling lane and a warp synchronization: 492). The main loop is unrolled by four blocks: rolled, branches
+// and instruction fetch cost 9% more.
 // Operand orientation: A and B are read K-major (contraction contiguous) or MN-major (output
 // index contiguous) straight from their row-major INT8 storage, so dgrad and wgrad re-block along
 // the other axis with no transpose pass.
 //
-// Ordering of the hand-offs: an accumulator is handed back only after tcgen05.wait::ld has returned
-// (its partials are in registers), and it is read only after its MMA's commit has been observed on
-// the mbarrier, so the barrier instructions themselves order the TMEM accesses; no tcgen05 fence is
-// issued per contraction block (only around the TMEM allocation and release).
+// Ordering of the hand-offs: a group is handed back only after tcgen05.wait::ld has returned (its partials
+// are in registers), and it is read only after its MMAs' commit has been observed on the mbarrier, so the
+// barrier instructions themselves order the TMEM accesses; no tcgen05 fence is issued per group (only
+// around the TMEM allocation and release). The two MMAs of a block have one shape and one accumulator,
+// so the tensor core runs them in order.
 //
 // Every mbarrier wait is bounded (ptx.cuh). On a timeout the warp that saw it sets the CTA's abort
-// flag; every warp then stops waiting and computing but keeps its place in the hardware-barrier
-// hand-offs (one per contraction block, always in the same order), so those complete; in-flight
-// copies and MMAs are drained (bounded) before TMEM is freed.
+// flag; every other wait then gives up too and the roles end; in-flight copies and MMAs are drained
+// (bounded) before TMEM is freed.
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -71,28 +71,39 @@ constexpr int BM = 128;             // tile rows = MMA M = TMEM lanes
 constexpr int BN = 128;             // tile cols = MMA N = TMEM columns of one accumulator
 constexpr int KB = 32;              // contraction block (one MMA, one rescale)
 constexpr int KBS = 4;              // contraction blocks per pipeline stage (128 bytes)
-constexpr int NBUF = 4;             // TMEM accumulators (4 x 128 = all 512 columns)
-constexpr int STAGES = 6;
-constexpr int NUM_MMA_WARPS = 2;    // alternate pipeline stages
-constexpr int FIRST_EPI_WARP = 1 + NUM_MMA_WARPS;
-constexpr int NUM_EPI_WARPS = 8;    // each owns two 32x32 output blocks of the 128 x 128 tile
-constexpr int WATCH_WARP = FIRST_EPI_WARP + NUM_EPI_WARPS;   // relays MMA completions to the epilogue
-constexpr int NUM_THREADS = 32 * (WATCH_WARP + 1);
-constexpr uint32_t HANDOFF_THREADS = 32 * (NUM_EPI_WARPS + 1);   // epilogue warps + one MMA warp
+constexpr int GROUP = 2;            // contraction blocks committed, waited for and handed back together
+constexpr int NGROUPS = 2;          // groups in TMEM (2 x 2 x 128 = all 512 columns)
+constexpr int STAGES = 4;
+constexpr int MMA_WARP = 1;
+constexpr int FIRST_SUM_WARP = 4;   // warps 2 and 3 have no role: the sum warps start a warpgroup
+constexpr int NUM_SUM_WARPS = 8;    // each owns two 32x32 output blocks of the 128 x 128 tile
+constexpr int FIRST_OUT_WARP = FIRST_SUM_WARP + NUM_SUM_WARPS;
+// Output warps take the sum warps' blocks through the tile's epilogue: 4 (two sum warps each), or 8 where a
+// tile's epilogue outlasts its main loop (launch_gemm). Registers: the threads start with an equal share;
+// the warpgroup of the producer and the MMA warp gives most of its own up, the sum warps take enough for 64
+// accumulators and 64 partials each, the output warps the rest. The shares' sum must not exceed the launch's
+// total, or setmaxnreg would wait for ever.
+template <int NOUT>
+struct Roles {
+  static constexpr int kThreads = 32 * (FIRST_OUT_WARP + NOUT);
+  static constexpr int kCtl = NOUT == 4 ? 40 : 24, kSum = NOUT == 4 ? 168 : 152, kOut = NOUT == 4 ? 136 : 72;
+  static constexpr int kLaunch = 65536 / kThreads / 8 * 8;
+  static_assert(128 * (kCtl + 2 * kSum) + 32 * NOUT * kOut <= kThreads * kLaunch, "register split");
+};
 constexpr int A_STAGE = BM * KBS * KB;  // 16 KB
 constexpr int B_STAGE = BN * KBS * KB;  // 16 KB
-constexpr uint32_t TMEM_COLS = NBUF * BN;
+constexpr uint32_t TMEM_COLS = NGROUPS * GROUP * BN;
+static_assert(KBS % GROUP == 0 && TMEM_COLS == 512, "groups do not cross pipeline stages and fill TMEM");
 
 constexpr int SMEM_A = 0;
 constexpr int SMEM_B = SMEM_A + STAGES * A_STAGE;
 constexpr int SMEM_BAR = SMEM_B + STAGES * B_STAGE;
-constexpr int NUM_BARS = 2 * STAGES + NBUF + NUM_MMA_WARPS;
+constexpr int NUM_BARS = 2 * STAGES + 2 * NGROUPS + 2 * NUM_SUM_WARPS + 1;
 constexpr int SMEM_MISC = SMEM_BAR + NUM_BARS * 8;
-constexpr int SMEM_STAGE = (SMEM_MISC + 16 + 127) / 128 * 128;   // the epilogue warps' staging areas
-constexpr int SMEM_BYTES = SMEM_STAGE + NUM_EPI_WARPS * kStageBytes + 1024;  // + slack to align the base to 1024
-// What a tile's epilogue does: the plain products, or a linear layer's forward / input gradient with
-// bias, activation and residual.
-enum Epilogue { kEpiPlain = 0, kEpiForward = 1, kEpiGrad = 2 };
+constexpr int SMEM_BIAS = (SMEM_MISC + 16 + 1023) / 1024 * 1024;   // 4 KB of -128: the operand of the bias MMA
+constexpr int SMEM_OUT = SMEM_BIAS + BM * KB;                      // the finished tile, 16 fp32 blocks of 4 KB
+constexpr int SMEM_BYTES = SMEM_OUT + BM * BN * 4 + 1024;          // + slack to align the base to 1024
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
 
 struct __align__(64) GemmParams {
   CUtensorMap tma_a;
@@ -101,27 +112,40 @@ struct __align__(64) GemmParams {
   const float* b_s;
   int64_t a_s_blk, a_s_k;  // scale of A at (row block r, contraction block kb): a_s[r*a_s_blk + kb*a_s_k]
   int64_t b_s_blk, b_s_k;
-  int8_t* y_q;
-  float* y_s;
-  float* y_f32;
-  int8_t* pre_q;
-  float* pre_s;
-  int act;
-  int64_t ld_y;
   unsigned int* status;
   int rows, cols, kblocks;
   int tiles_m, tiles_n;
   int n_fast;   // tile order: 0 = row tiles vary fastest, 1 = column tiles vary fastest
-  EpilogueParams ep;   // kEpiForward / kEpiGrad only
+  EpilogueParams ep;
 };
 
-// Row and column tile of the CTA's tile t. The 148 tiles in flight at once share one operand's
-// blocks: with row tiles varying fastest they cover nearly all row tiles (all of A) and a few
-// column tiles, so A is re-read from L2 by every wave and B streams once; the host picks the order
-// that keeps the smaller operand the re-read one, so that it stays in L2.
-__device__ __forceinline__ int2 tile_of(const GemmParams& p, int t) {
-  return p.n_fast ? make_int2(t / p.tiles_n, t % p.tiles_n) : make_int2(t % p.tiles_m, t / p.tiles_m);
-}
+// The CTA's tiles t = blockIdx.x, blockIdx.x + gridDim.x, ... in order, as row and column tiles. The 148
+// tiles in flight at once share one operand's blocks: with row tiles varying fastest they cover nearly
+// all row tiles (all of A) and a few column tiles, so A is re-read from L2 by every wave and B streams
+// once; the host picks the order that keeps the smaller operand the re-read one, so that it stays in L2.
+// Two divisions at the start and additions from tile to tile: divided anew for every tile, the
+// coordinates took each sum warp ~1000 cycles between two tiles.
+struct TileWalk {
+  int a, b, da, db, na;   // tile t = b na + a, a varying fastest
+  bool n_fast;
+  __device__ __forceinline__ explicit TileWalk(const GemmParams& p)
+      : na(p.n_fast ? p.tiles_n : p.tiles_m), n_fast(p.n_fast != 0) {
+    a = int(blockIdx.x) % na;
+    b = int(blockIdx.x) / na;
+    da = int(gridDim.x) % na;
+    db = int(gridDim.x) / na;
+  }
+  __device__ __forceinline__ void next() {
+    a += da;
+    b += db;
+    if (a >= na) {
+      a -= na;
+      ++b;
+    }
+  }
+  __device__ __forceinline__ int row() const { return n_fast ? b : a; }
+  __device__ __forceinline__ int col() const { return n_fast ? a : b; }
+};
 
 // tcgen05 instruction descriptor: s32 accumulator, signed int8 A and B, A/B major-ness, N, M.
 template <bool A_MN, bool B_MN, int N>
@@ -136,20 +160,33 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
          (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
+// The partial sums' encoding. An MMA of constant operands first sets every accumulator to
+// 32 * 128 * 128 = 2^19, and the block's own MMA adds its exact partial P on top (|P| <= 2^19), so an
+// accumulator holds n = P + 2^19 in [0, 2^20]. Read as an fp32 bit pattern that is the denormal number
+// n 2^-149, and one FMA, n 2^-149 * 2^126 - 2^-4, is exactly P 2^-23: the conversion runs in the FMA pipe, two
+// values per packed instruction, and not as one int -> float conversion per value. Those cost more than
+// their own issue slots: while both sum warps of the MMA warp's sub-partition convert, its tcgen05
+// instructions take 327 cycles each instead of 87.
+constexpr float kSumScale = 8388608.0f;            // 2^23, multiplied into the block's scale (exact)
+__device__ __forceinline__ void partial_x2(uint32_t r0, uint32_t r1, float& f0, float& f1) {
+  constexpr float k126 = 8.507059173023461587e37f;   // 2^126
+  fma_x2(__uint_as_float(r0), __uint_as_float(r1), k126, k126, -0.0625f, -0.0625f, f0, f1);
+}
 
-// Re-quantize one warp's 32x32 fp32 block (lane = row; the row's 32 values in acc) and store its
-// codes at q (lane's row, ld_y-strided by the caller's offset) and its scale at *s.
-__device__ __forceinline__ void store_block_q(const float (&acc)[32], int8_t* q, float* s, const int lane) {
-  float m = 0.0f;
+// A finished block between a sum warp and an output warp: row = lane, 16-byte chunk c of a row at position
+// c ^ (row % 8) (conflict-free both ways).
+__device__ __forceinline__ void block_to_smem(const float (&v)[32], uint8_t* blk, int lane) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(acc[i]));
-  const BlockQuant bq = block_quant(warp_max_nonneg(m));
-  uint32_t w[8];
-  quant_pack<32>(acc, bq, w);
-  uint4* dst = reinterpret_cast<uint4*>(q);
-  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  if (lane == 0) *s = bq.s;
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<float4*>(blk + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+        make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+}
+__device__ __forceinline__ void block_from_smem(float (&v)[32], const uint8_t* blk, int lane) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const float4 f = *reinterpret_cast<const float4*>(blk + lane * 128 + ((c ^ (lane & 7)) << 4));
+    v[4 * c] = f.x; v[4 * c + 1] = f.y; v[4 * c + 2] = f.z; v[4 * c + 3] = f.w;
+  }
 }
 
 // The 32 scales of one operand's row (or column) block `blk` for contraction blocks w0 .. w0+31:
@@ -160,16 +197,19 @@ __device__ __forceinline__ float scale_window(const float* __restrict__ base, in
   return (blk < nblk && kb < kblocks) ? __ldg(base + blk * s_blk + int64_t(kb) * s_k) : 0.0f;
 }
 
-template <bool A_MN, bool B_MN, int EPI>
-__global__ void __launch_bounds__(NUM_THREADS, 1) gemm_i8_kernel(const __grid_constant__ GemmParams p) {
+template <bool A_MN, bool B_MN, int EPI, int NOUT>
+__global__ void __launch_bounds__(Roles<NOUT>::kThreads, 1) gemm_i8_kernel(const __grid_constant__ GemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem + SMEM_A;
   uint8_t* sB = smem + SMEM_B;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SMEM_BAR);  // per stage: A and B landed
   uint64_t* empty = full + STAGES;      // per stage: the MMAs that read it completed
-  uint64_t* tfull = empty + STAGES;     // per accumulator: its MMA completed
-  uint64_t* drain = tfull + NBUF;
+  uint64_t* tfull = empty + STAGES;     // per group: its MMAs completed
+  uint64_t* tempty = tfull + NGROUPS;   // per group: every epilogue warp has read it
+  uint64_t* ofull = tempty + NGROUPS;         // per sum warp: its two finished blocks are in shared memory
+  uint64_t* oempty = ofull + NUM_SUM_WARPS;   // per sum warp: they have been written out
+  uint64_t* drain = oempty + NUM_SUM_WARPS;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + SMEM_MISC);
   volatile uint32_t* abort_flag = tmem_holder + 1;
 
@@ -179,8 +219,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_i8_kernel(const __grid_co
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < NBUF; ++b) mbar_init(&tfull[b], 1);
-    for (int m = 0; m < NUM_MMA_WARPS; ++m) mbar_init(&drain[m], 1);
+    for (int b = 0; b < NGROUPS; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], NUM_SUM_WARPS);
+    }
+    for (int w = 0; w < NUM_SUM_WARPS; ++w) {
+      mbar_init(&ofull[w], 1);
+      mbar_init(&oempty[w], 1);
+    }
+    mbar_init(drain, 1);
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -195,6 +242,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_i8_kernel(const __grid_co
     tmem_alloc(tmem_holder, TMEM_COLS);
     tmem_relinquish();
   }
+  for (int i = threadIdx.x; i < BM * KB / 4; i += Roles<NOUT>::kThreads) reinterpret_cast<uint32_t*>(smem + SMEM_BIAS)[i] = 0x80808080u;
+  fence_proxy_async_smem();   // the bias operand is read by the tensor core
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -205,198 +254,191 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) gemm_i8_kernel(const __grid_co
   const int num_tiles = p.tiles_m * p.tiles_n;
   const int my_tiles = blockIdx.x < num_tiles ? (num_tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
   const int total_stages = my_tiles * num_kstages;   // this CTA's stages, in order
-  const int total = my_tiles * kblocks;              // this CTA's contraction blocks, in order
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ producer warp
-    if (lane == 0) {
-      uint32_t pending = 0, pend_ph = 0;  // slots armed, and the parity armed
-      for (int g = 0; g < total_stages; ++g) {
-        const int t = blockIdx.x + (g / num_kstages) * gridDim.x;
-        const int ks = g % num_kstages;
-        const int2 tc = tile_of(p, t);
-        const int row0 = tc.x * BM, col0 = tc.y * BN;
-        const int st = g % STAGES;
-        const uint32_t ph = uint32_t(g / STAGES) & 1u;
-        if (!mbar_wait(&empty[st], ph ^ 1u, abort_flag, p.status)) break;
-        mbar_arrive_expect_tx(&full[st], A_STAGE + B_STAGE);
-        pending |= 1u << st;
-        pend_ph = (pend_ph & ~(1u << st)) | (ph << st);
-        const int k0 = ks * KBS * KB;
-        if (!A_MN) tma_load_2d(sA + st * A_STAGE, &p.tma_a, &full[st], k0, row0);
-        else tma_load_2d(sA + st * A_STAGE, &p.tma_a, &full[st], row0, k0);
-        if (!B_MN) tma_load_2d(sB + st * B_STAGE, &p.tma_b, &full[st], k0, col0);
-        else tma_load_2d(sB + st * B_STAGE, &p.tma_b, &full[st], col0, k0);
-      }
-      // Teardown: every copy issued has landed before the CTA exits.
-      for (int s = 0; s < STAGES; ++s)
-        if (pending & (1u << s)) mbar_wait_teardown(&full[s], (pend_ph >> s) & 1u, p.status);
-    }
-    __syncwarp();
-  } else if (warp < FIRST_EPI_WARP) {
-    // ------------------------------------------------------------------ MMA warps
-    // Warp 1 + m issues the MMAs of the CTA's pipeline stages s = m, m + 2, ... (each stage's four
-    // contraction blocks, in order). Before the MMA of contraction block G (G >= NBUF) it waits on
-    // hardware barrier hand_bar(G) until every epilogue warp has read accumulator G % NBUF, i.e.
-    // block G - NBUF. The two warps use disjoint barriers, so each barrier's phases are only ever
-    // waited on by one warp, in order; each warp commits its own stages' `empty` barriers.
-    constexpr uint32_t idesc = instr_desc<A_MN, B_MN, BN>();
-    const int m = warp - 1;
-    bool dead = false, issued = false;
-    for (int s = m; s < total_stages; s += NUM_MMA_WARPS) {
-      const int ks = s % num_kstages;
-      const int g0 = (s / num_kstages) * kblocks + ks * KBS;
-      const int nk = min(KBS, kblocks - ks * KBS);
-      const int slot = s % STAGES;
-      for (int kk = 0; kk < nk; ++kk) {
-        const int G = g0 + kk;
-        const uint32_t b = uint32_t(G) & (NBUF - 1);
-        if (G >= NBUF) named_bar_sync(1 + b + NBUF * m, HANDOFF_THREADS);   // block G - NBUF was read
-        if (lane == 0) {
-          if (kk == 0 && !dead) dead = !mbar_wait(&full[slot], uint32_t(s / STAGES) & 1u, abort_flag, p.status);
-          // after a timeout every block's barrier is still completed (plain arrive), so the watcher
-          // and the epilogue keep their order and finish
-          if (dead) mbar_arrive(&tfull[b]);
-          if (!dead) {
-            const uint32_t a_addr = smem_u32(sA + slot * A_STAGE);
-            const uint32_t b_addr = smem_u32(sB + slot * B_STAGE);
-            // K-major: the 32-byte K step moves inside the 128-byte swizzle row;
-            // MN-major: it moves by 32 rows of 128 bytes (four 8-row swizzle atoms).
-            const uint64_t ad = smem_desc(a_addr + (A_MN ? kk * 4096 : kk * 32), A_MN ? 16384 : 16, 1024);
-            const uint64_t bd = smem_desc(b_addr + (B_MN ? kk * 4096 : kk * 32), B_MN ? 16384 : 16, 1024);
-            mma_i8(tmem_base + b * BN, ad, bd, idesc, 0u);
-            tc_commit(&tfull[b]);
-            issued = true;
+  if (warp < FIRST_SUM_WARP) {
+    setmaxnreg_dec<Roles<NOUT>::kCtl>();
+    if (warp == 0) {
+      // ------------------------------------------------------------------ producer warp
+      if (lane == 0) {
+        uint32_t pending = 0, pend_ph = 0;  // slots armed, and the parity armed
+        TileWalk at(p);
+        int ks = 0, st = 0;
+        uint32_t ph = 0;
+        for (int g = 0; g < total_stages; ++g) {
+          const int row0 = at.row() * BM, col0 = at.col() * BN;
+          // far ahead of the MMAs: it looks now and then instead of polling beside the warps at work
+          for (int i = 0; i < 4096 && !mbar_try_wait(&empty[st], ph ^ 1u); ++i) __nanosleep(300);
+          if (!mbar_wait(&empty[st], ph ^ 1u, abort_flag, p.status)) break;
+          mbar_arrive_expect_tx(&full[st], A_STAGE + B_STAGE);
+          pending |= 1u << st;
+          pend_ph = (pend_ph & ~(1u << st)) | (ph << st);
+          const int k0 = ks * KBS * KB;
+          if (!A_MN) tma_load_2d(sA + st * A_STAGE, &p.tma_a, &full[st], k0, row0);
+          else tma_load_2d(sA + st * A_STAGE, &p.tma_a, &full[st], row0, k0);
+          if (!B_MN) tma_load_2d(sB + st * B_STAGE, &p.tma_b, &full[st], k0, col0);
+          else tma_load_2d(sB + st * B_STAGE, &p.tma_b, &full[st], col0, k0);
+          if (++ks == num_kstages) {
+            ks = 0;
+            at.next();
+          }
+          if (++st == STAGES) {
+            st = 0;
+            ph ^= 1u;
           }
         }
-        __syncwarp();
+        // Teardown: every copy issued has landed before the CTA exits.
+        for (int s = 0; s < STAGES; ++s)
+          if (pending & (1u << s)) mbar_wait_teardown(&full[s], (pend_ph >> s) & 1u, p.status);
       }
-      if (lane == 0 && !dead) tc_commit(&empty[slot]);   // the slot may be refilled once these MMAs complete
+      __syncwarp();
+    } else if (warp == MMA_WARP) {
+      // ------------------------------------------------------------------ MMA warp
+      if (lane == 0) {
+        constexpr uint32_t idesc = instr_desc<A_MN, B_MN, BN>();
+        // K-major: the 32-byte K step moves inside the 128-byte swizzle row;
+        // MN-major: it moves by 32 rows of 128 bytes (four 8-row swizzle atoms).
+        // The descriptors differ in their address field alone (16-byte units, low word).
+        const uint64_t ad0 = smem_desc(smem_u32(sA), A_MN ? 16384 : 16, 1024);
+        const uint64_t bd0 = smem_desc(smem_u32(sB), B_MN ? 16384 : 16, 1024);
+        const uint32_t a_lo = uint32_t(ad0), a_hi = uint32_t(ad0 >> 32), b_lo = uint32_t(bd0), b_hi = uint32_t(bd0 >> 32);
+        constexpr uint32_t a_step = (A_MN ? 4096 : 32) / 16, b_step = (B_MN ? 4096 : 32) / 16;
+        // every byte of the bias operand is -128, so any descriptor inside its 4 KB describes it (no swizzle)
+        const uint64_t bias = uint64_t((smem_u32(smem + SMEM_BIAS) >> 4) & 0x3FFFu) | (uint64_t(128 >> 4) << 16) |
+                              (uint64_t(256 >> 4) << 32) | (uint64_t(1) << 46);
+        constexpr uint32_t bias_idesc = instr_desc<false, false, BN>();
+        bool ok = true, issued = false;
+        int gi = 0, slot = 0, left = kblocks;       // groups so far: group gi lives in TMEM half gi % 2
+        uint32_t sph = 0;
+        for (int s = 0; ok && s < total_stages; ++s) {
+          if (!mbar_wait(&full[slot], sph, abort_flag, p.status)) break;
+          const int nk = min(KBS, left);
+          uint32_t a = a_lo + slot * (A_STAGE / 16), bb = b_lo + slot * (B_STAGE / 16);
+#pragma unroll
+          for (int kk = 0; kk < KBS; kk += GROUP) {
+            if (kk >= nk) break;
+            const uint32_t b = uint32_t(gi) & 1u;
+            if (!mbar_wait(&tempty[b], (uint32_t(gi >> 1) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
+            const uint32_t d = tmem_base + b * (GROUP * BN);
+            mma_i8(d, bias, bias, bias_idesc, 0u);
+            if (kk + 1 < nk) mma_i8(d + BN, bias, bias, bias_idesc, 0u);
+            mma_i8_add(d, a + kk * a_step, a_hi, bb + kk * b_step, b_hi, idesc);
+            if (kk + 1 < nk) mma_i8_add(d + BN, a + (kk + 1) * a_step, a_hi, bb + (kk + 1) * b_step, b_hi, idesc);
+            tc_commit(&tfull[b]);
+            issued = true;
+            ++gi;
+          }
+          if (ok) tc_commit(&empty[slot]);   // the slot may be refilled once these MMAs complete
+          if (++slot == STAGES) { slot = 0; sph ^= 1u; }
+          left -= KBS;
+          if (left <= 0) left = kblocks;
+        }
+        // Teardown: no MMA may still be writing TMEM when it is freed.
+        if (issued) {
+          tc_commit(drain);
+          mbar_wait_teardown(drain, 0u, p.status);
+        }
+      }
       __syncwarp();
     }
-    // The last NBUF hand-offs precede no MMA; warp 1 takes them so that every phase completes.
-    if (m == 0)
-      for (int G = max(total, NBUF); G < total + NBUF; ++G) named_bar_sync(1 + (uint32_t(G) & (NBUF - 1)), HANDOFF_THREADS);
-    // Teardown: no MMA may still be writing TMEM when it is freed.
-    if (lane == 0 && issued) {
-      tc_commit(&drain[m]);
-      mbar_wait_teardown(&drain[m], 0u, p.status);
-    }
-    __syncwarp();
-  } else if (warp == WATCH_WARP) {
-    // ------------------------------------------------------------------ completion watcher
-    // The only thread that polls the accumulators' mbarriers: once block g's MMA has completed it
-    // releases the epilogue warps through hardware barrier 9 + g % NBUF (they wait there with
-    // bar.sync, without polling).
-    // Every block's barrier completes, by its MMA's commit or, after a timeout elsewhere, by the MMA
-    // warp's plain arrive, so this wait ignores the abort flag; its limit (three watchdog periods)
-    // outlasts every other bounded wait. Should it still run out, the watcher waits on the release
-    // barrier itself (bar.sync) from then on, so it never runs ahead of the epilogue warps.
-    uint32_t never = 0u;
-    bool lost = false;
-    for (int g = 0; g < total; ++g) {
-      const uint32_t b = uint32_t(g) & (NBUF - 1);
-      bool good = true;
-      if (lane == 0 && !lost) {
-        const uint32_t ph = uint32_t(g / NBUF) & 1u;
-        good = mbar_try_wait(&tfull[b], ph) || mbar_wait(&tfull[b], ph, &never, p.status, 3 * kWatchdogNs);
-      }
-      lost = lost || !__shfl_sync(0xffffffffu, good, 0);
-      if (lost) named_bar_sync(9 + b, HANDOFF_THREADS);
-      else named_bar_arrive(9 + b, HANDOFF_THREADS);
-    }
-  } else {
-    // ------------------------------------------------------------------ epilogue warps
+  } else if (warp < FIRST_OUT_WARP) {
+    // ------------------------------------------------------------------ sum warps
+    setmaxnreg_inc<Roles<NOUT>::kSum>();
+    const int w = warp - FIRST_SUM_WARP;
     const int sub = warp & 3;             // TMEM sub-partition this warp may access = row block in the tile
-    const int cb0 = ((warp - FIRST_EPI_WARP) >> 2) * 2;  // first of the warp's two column blocks in the tile
+    const int cb0 = (w >> 2) * 2;         // first of the warp's two column blocks in the tile
     const uint32_t t_base = tmem_base + (uint32_t(sub * 32) << 16) + uint32_t(cb0 * 32);
     const int nrb = p.rows >> 5, ncb = p.cols >> 5;
-    const bool whole_stages = (kblocks % KBS) == 0;   // then every stage holds KBS blocks
     // Scales of the current window (lane l: contraction block w0 + l) of the warp's row block (sa)
     // and two column blocks (sb0, sb1); each window prefetches the next one.
     float sa_n, sb0_n, sb1_n;
-    auto load_scales = [&](int t, int w0, bool valid) {
-      const int2 tc = tile_of(p, t);
-      const int rbk = tc.x * (BM / 32) + sub, cbk = tc.y * (BN / 32) + cb0;
+    auto load_scales = [&](const TileWalk& at, int w0, bool valid) {
+      const int rbk = at.row() * (BM / 32) + sub, cbk = at.col() * (BN / 32) + cb0;
       sa_n = scale_window(p.a_s, p.a_s_blk, p.a_s_k, rbk, valid ? nrb : 0, w0, kblocks, lane);
       sb0_n = scale_window(p.b_s, p.b_s_blk, p.b_s_k, cbk, valid ? ncb : 0, w0, kblocks, lane);
       sb1_n = scale_window(p.b_s, p.b_s_blk, p.b_s_k, cbk + 1, valid ? ncb : 0, w0, kblocks, lane);
     };
-    load_scales(blockIdx.x, 0, my_tiles > 0);
-    int g = 0;                            // contraction blocks consumed so far (accumulator g % NBUF)
+    TileWalk at(p);                       // the tile of the scales loaded last
+    load_scales(at, 0, my_tiles > 0);
+    int gi = 0;                           // groups consumed so far
+    bool alive = true;
     for (int tile = 0; tile < my_tiles; ++tile) {
-      const int t = blockIdx.x + tile * gridDim.x;
-      const int2 tc = tile_of(p, t);
-      const int rbk = tc.x * (BM / 32) + sub, cbk = tc.y * (BN / 32) + cb0;
       float acc[2][32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acc[0][i] = acc[1][i] = 0.0f;
-      for (int w0 = 0; w0 < kblocks; w0 += 32) {
-        // lane l: fp32(sA * sB) of contraction block w0 + l for the warp's two output blocks
-        const float cw0 = sa_n * sb0_n, cw1 = sa_n * sb1_n;
-        if (w0 + 32 < kblocks) load_scales(t, w0 + 32, true);   // the rest of this tile
-        else load_scales(t + gridDim.x, 0, tile + 1 < my_tiles);  // the start of the next one
+      for (int w0 = 0; alive && w0 < kblocks; w0 += 32) {
+        // lane l: fp32(sA * sB) of contraction block w0 + l for the warp's two output blocks, times 2^23 (exact)
+        const float cw0 = sa_n * sb0_n * kSumScale, cw1 = sa_n * sb1_n * kSumScale;
+        const bool more = w0 + 32 < kblocks;   // the rest of this tile, or the start of the next one
+        if (!more) at.next();
+        load_scales(at, more ? w0 + 32 : 0, more || tile + 1 < my_tiles);
         const int nk = min(32, kblocks - w0);
-        // two blocks per iteration: measured 7-9% faster than one, bit-identical; four spill registers
-#pragma unroll 2
-        for (int j = 0; j < nk; ++j, ++g) {
-          const uint32_t b = uint32_t(g) & (NBUF - 1);
+        // one contraction block: TMEM -> registers, then acc += c P (packed fp32x2 FMAs, each lane rounded
+        // as the scalar fmaf); `last`: the group is in registers and its accumulators may be overwritten
+        auto block = [&](uint32_t b, int k, int j, bool last) {
           uint32_t r[64];
-          named_bar_sync(9 + b, HANDOFF_THREADS);   // the watcher saw block g's MMA complete
-          tmem_ld_32x32b_x64(t_base + b * BN, r);
-          tc_wait_ld64(r);   // the partials are in registers: the MMA may overwrite the accumulator
-          {  // hand accumulator b back: the barrier of the MMA warp of block g + NBUF (the warp of that
-             // block's stage; warp 1 takes the hand-offs past the last block)
-            const int G = g + NBUF;
-            int sn = 0;
-            if (G < total) {
-              if (whole_stages) {
-                sn = G / KBS;
-              } else {
-                const int kn = w0 + j + NBUF;   // tile-local index of block G
-                sn = kn < kblocks ? tile * num_kstages + kn / KBS : (G / kblocks) * num_kstages + (G % kblocks) / KBS;
-              }
-            }
-            named_bar_arrive(1 + b + NBUF * uint32_t(sn % NUM_MMA_WARPS), HANDOFF_THREADS);
-          }
+          tmem_ld_32x32b_x64(t_base + (b * GROUP + k) * BN, r);
           const float c0 = __shfl_sync(0xffffffffu, cw0, j), c1 = __shfl_sync(0xffffffffu, cw1, j);
+          tc_wait_ld64(r);
+          if (last) mbar_arrive_if(&tempty[b], lane == 0);
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {   // packed fp32x2 FMAs, each lane rounded as the scalar fmaf
-            fma_x2(c0, c0, __int2float_rn(int(r[i])), __int2float_rn(int(r[i + 1])), acc[0][i], acc[0][i + 1],
-                   acc[0][i], acc[0][i + 1]);
-            fma_x2(c1, c1, __int2float_rn(int(r[32 + i])), __int2float_rn(int(r[33 + i])), acc[1][i], acc[1][i + 1],
-                   acc[1][i], acc[1][i + 1]);
+          for (int i = 0; i < 32; i += 2) {
+            float f0, f1, f2, f3;
+            partial_x2(r[i], r[i + 1], f0, f1);
+            partial_x2(r[32 + i], r[33 + i], f2, f3);
+            fma_x2(c0, c0, f0, f1, acc[0][i], acc[0][i + 1], acc[0][i], acc[0][i + 1]);
+            fma_x2(c1, c1, f2, f3, acc[1][i], acc[1][i + 1], acc[1][i], acc[1][i + 1]);
           }
+        };
+        int j0 = 0;
+#pragma unroll 2
+        for (; j0 + GROUP <= nk; j0 += GROUP, ++gi) {
+          const uint32_t b = uint32_t(gi) & 1u;
+          const bool good = mbar_wait_often(&tfull[b], uint32_t(gi >> 1) & 1u, abort_flag, p.status);
+          if (!__all_sync(0xffffffffu, good)) { alive = false; break; }
+          block(b, 0, j0, false);
+          block(b, 1, j0 + 1, true);
+        }
+        if (alive && j0 < nk) {           // the odd block at the end of a tile
+          const uint32_t b = uint32_t(gi) & 1u;
+          const bool good = mbar_wait_often(&tfull[b], uint32_t(gi >> 1) & 1u, abort_flag, p.status);
+          alive = __all_sync(0xffffffffu, good);
+          if (alive) block(b, 0, j0, true);
+          ++gi;
         }
       }
-
-      if constexpr (EPI != kEpiPlain) {
-        if (rbk < nrb && cbk < ncb)
-          linear_epilogue<EPI == kEpiGrad>(p.ep, p.act, acc, p.y_q, p.y_s, p.pre_q, p.pre_s, p.ld_y, rbk, cbk, ncb,
-                                           cbk + 1 < ncb, smem + SMEM_STAGE + (warp - FIRST_EPI_WARP) * kStageBytes, lane);
-      } else {
-        // ---- on-chip re-quantization of this warp's two 32x32 blocks of the finished tile (the loop is
-        // unrolled so that acc stays in registers)
+      if (!alive) break;
+      // the finished blocks to the output warps, and on to the next tile
+      const bool room = mbar_wait_often(&oempty[w], (uint32_t(tile) & 1u) ^ 1u, abort_flag, p.status);
+      if (!__all_sync(0xffffffffu, room)) break;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (rbk >= nrb || cbk + h >= ncb) continue;
-          float (&y)[32] = acc[h];
-          const int64_t off = (int64_t(rbk) * 32 + lane) * p.ld_y + int64_t(cbk + h) * 32;
-          const int64_t soff = int64_t(rbk) * ncb + cbk + h;
-          if (p.act == kActGelu) {
-            // fused activation: the fp32 pre-activation is re-quantized (when asked for) and GELU is
-            // applied to it on chip, so neither ever makes an HBM round trip in fp32
-            if (p.pre_q != nullptr) store_block_q(y, p.pre_q + off, p.pre_s + soff, lane);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) y[i] = gelu_f32(y[i]);
-          }
-          if (p.y_q != nullptr) store_block_q(y, p.y_q + off, p.y_s + soff, lane);
-          if (p.y_f32 != nullptr) {
-            float4* dst = reinterpret_cast<float4*>(p.y_f32 + off);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-          }
+      for (int h = 0; h < 2; ++h) block_to_smem(acc[h], smem + SMEM_OUT + (2 * w + h) * 4096, lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ofull[w]);
+    }
+  } else {
+    // ------------------------------------------------------------------ output warps
+    if constexpr (Roles<NOUT>::kOut > Roles<NOUT>::kLaunch) setmaxnreg_inc<Roles<NOUT>::kOut>();
+    else setmaxnreg_dec<Roles<NOUT>::kOut>();
+    const int nrb = p.rows >> 5, ncb = p.cols >> 5;
+    TileWalk at(p);
+    bool alive = true;
+    for (int tile = 0; alive && tile < my_tiles; ++tile, at.next()) {
+      for (int w = warp - FIRST_OUT_WARP; w < NUM_SUM_WARPS; w += NOUT) {
+        const bool good = mbar_wait_often(&ofull[w], uint32_t(tile) & 1u, abort_flag, p.status);
+        alive = __all_sync(0xffffffffu, good);
+        if (!alive) break;
+        const int rbk = at.row() * (BM / 32) + (w & 3), cbk = at.col() * (BN / 32) + (w >> 2) * 2;
+        const int nblk = rbk < nrb ? min(2, ncb - cbk) : 0;
+#pragma unroll 1
+        for (int h = 0; h < nblk; ++h) {
+          uint8_t* blk = smem + SMEM_OUT + (2 * w + h) * 4096;
+          float v[32];
+          block_from_smem(v, blk, lane);
+          __syncwarp();                   // the block's memory is the warp's staging area from here on
+          block_epilogue<EPI>(p.ep, v, rbk, cbk + h, ncb, blk, lane);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&oempty[w]);
       }
     }
   }
@@ -582,10 +624,10 @@ static bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool A_MN, bool B_MN, int EPI>
+template <bool A_MN, bool B_MN, int EPI, int NOUT>
 static cudaError_t run(const GemmParams& prm, int grid, cudaStream_t st) {
   static unsigned long long attr_set = 0;  // one bit per device ordinal
-  auto kern = gemm_i8_kernel<A_MN, B_MN, EPI>;
+  auto kern = gemm_i8_kernel<A_MN, B_MN, EPI, NOUT>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -595,7 +637,7 @@ static cudaError_t run(const GemmParams& prm, int grid, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     attr_set |= bit;
   }
-  kern<<<grid, NUM_THREADS, SMEM_BYTES, st>>>(prm);
+  kern<<<grid, Roles<NOUT>::kThreads, SMEM_BYTES, st>>>(prm);
   return cudaGetLastError();
 }
 
@@ -603,7 +645,6 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t st) {
   GemmParams prm;
   memset(&prm, 0, sizeof(prm));
   const int64_t rb = g.rows / 32, cb = g.cols / 32, kbn = g.depth / 32;
-  bool a_mn = false, b_mn = false;
   bool okA = true, okB = true;
   const bool operands = g.depth > 0;   // without a contraction (bias and residual alone) nothing is loaded
   switch (g.mode) {
@@ -614,14 +655,12 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t st) {
       prm.b_s_blk = kbn; prm.b_s_k = 1;
       break;
     case kDgrad:  // A = dY [rows, depth] K-major; B = W [depth, cols] MN-major
-      b_mn = true;
       okA = !operands || make_map(&prm.tma_a, g.a_q, g.depth, g.rows, g.a_ld, 128, BM);
       okB = !operands || make_map(&prm.tma_b, g.b_q, g.cols, g.depth, g.b_ld, 128, 128);
       prm.a_s_blk = kbn; prm.a_s_k = 1;
       prm.b_s_blk = 1; prm.b_s_k = cb;
       break;
     default:  // kWgrad: A = dY [depth, rows] MN-major; B = X [depth, cols] MN-major
-      a_mn = b_mn = true;
       okA = !operands || make_map(&prm.tma_a, g.a_q, g.rows, g.depth, g.a_ld, 128, 128);
       okB = !operands || make_map(&prm.tma_b, g.b_q, g.cols, g.depth, g.b_ld, 128, 128);
       prm.a_s_blk = 1; prm.a_s_k = rb;
@@ -631,13 +670,6 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t st) {
   if (!okA || !okB) return cudaErrorInvalidValue;
   prm.a_s = g.a_s;
   prm.b_s = g.b_s;
-  prm.y_q = g.y_q;
-  prm.y_s = g.y_s;
-  prm.y_f32 = g.y_f32;
-  prm.act = g.act;
-  prm.pre_q = g.pre_q;
-  prm.pre_s = g.pre_s;
-  prm.ld_y = g.cols;
   prm.status = g.status;
   prm.rows = int(g.rows);
   prm.cols = int(g.cols);
@@ -647,24 +679,34 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t st) {
   prm.tiles_n = int((g.cols + BN - 1) / BN);
   const int tiles = prm.tiles_m * prm.tiles_n;
   const int grid = tiles < sm_count ? tiles : sm_count;
-  if (g.ep != nullptr) {
-    const auto bytes = [](int type) { return int64_t(type == kDenseF32 ? 4 : 2); };
-    const GemmEpilogue& e = *g.ep;
-    prm.ep.bias = e.bias;
-    prm.ep.act_q = e.act_q;
-    prm.ep.act_s = e.act_s;
-    prm.ep.res = static_cast<const uint8_t*>(e.res);
-    prm.ep.res_s = e.res_s;
-    prm.ep.res_type = e.res_type;
-    prm.ep.res_ld = e.res_ld * bytes(e.res_type);
-    prm.ep.y = static_cast<uint8_t*>(e.y);
-    prm.ep.y_type = e.y_type;
-    prm.ep.y_ld = e.y_ld * bytes(e.y_type);
-    return b_mn ? run<false, true, kEpiGrad>(prm, grid, st) : run<false, false, kEpiForward>(prm, grid, st);
-  }
-  if (!a_mn && !b_mn) return run<false, false, kEpiPlain>(prm, grid, st);
-  if (!a_mn && b_mn) return run<false, true, kEpiPlain>(prm, grid, st);
-  return run<true, true, kEpiPlain>(prm, grid, st);
+  const auto bytes = [](int type) { return int64_t(type == kDenseF32 ? 4 : 2); };
+  prm.ep.bias = g.bias;
+  prm.ep.act = g.act;
+  prm.ep.act_q = g.act_q;
+  prm.ep.act_s = g.act_s;
+  prm.ep.res = static_cast<const uint8_t*>(g.res);
+  prm.ep.res_s = g.res_s;
+  prm.ep.res_type = g.res_type;
+  prm.ep.res_ld = g.res_ld * bytes(g.res_type);
+  prm.ep.y_q = g.y_q;
+  prm.ep.y_s = g.y_s;
+  prm.ep.pre_q = g.pre_q;
+  prm.ep.pre_s = g.pre_s;
+  prm.ep.ld_q = g.cols;
+  prm.ep.y = static_cast<uint8_t*>(g.y);
+  prm.ep.y_type = g.y_type;
+  prm.ep.y_ld = g.y_ld * bytes(g.y_type);
+  // An epilogue with two re-quantizations, an activation gradient or the exact GELU takes 4 output warps about
+  // as long as 64 contraction blocks of main loop: below that 8 of them are faster (4096 x 1024 x 4096 with
+  // GELU and both outputs 103 us against 111, its input gradient 92 against 102), above they only slow the sum
+  // warps down (8192 x 16384 x 4096 1792 us against 1727).
+  const bool long_epilogue = g.pre_q != nullptr || g.act == kActGelu || (g.mode == kDgrad && g.act != kActNone);
+  const bool out8 = long_epilogue && kbn <= 64;
+  if (g.mode == kFwd)
+    return out8 ? run<false, false, kEpiForward, 8>(prm, grid, st) : run<false, false, kEpiForward, 4>(prm, grid, st);
+  if (g.mode == kDgrad)
+    return out8 ? run<false, true, kEpiGrad, 8>(prm, grid, st) : run<false, true, kEpiGrad, 4>(prm, grid, st);
+  return run<true, true, kEpiPlain, 4>(prm, grid, st);
 }
 
 cudaError_t launch_gemm_s32(const int8_t* a, const int8_t* b, int32_t* c, int64_t M, int64_t N, int64_t K,

@@ -98,24 +98,11 @@ cudaError_t launch_rope_table(const double* inv_freq, int64_t half, double magni
 // fp32(sA(r/32, kb) * sB(c/32, kb)) * sum_{k in kb} A(r, k) B(c, k), re-quantized per 32x32 block.
 // The operand views differ per mode (see gemm.cu).
 enum GemmMode { kFwd = 0, kDgrad = 1, kWgrad = 2 };
-enum GemmAct { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+// kActGelu is the GELU of jf_linear_fwd_gelu (gelu_f32), kActGeluEpi that of the epilogue calls (jf_activation's
+// JF_ACT_GELU, gelu_epilogue_x2): the same function and fit, evaluated with fewer instructions.
+enum GemmAct { kActNone = 0, kActRelu = 1, kActGeluEpi = 2, kActGeluTanh = 3, kActSilu = 4, kActGelu = 5 };
 // Element type of a dense matrix (jf_dtype's values) or an INT8 residual.
 enum DenseType { kDenseF32 = 0, kDenseBf16 = 1, kDenseF16 = 2, kResI8 = 3 };
-
-// The parts of a linear layer's epilogue beyond the product (see epilogue.cuh): what the forward and the
-// input-gradient calls with bias / activation / residual add to GemmArgs. Null pointers are absent parts.
-struct GemmEpilogue {
-  const float* bias;          // forward: fp32 [cols]
-  const int8_t* act_q;        // input gradient: the saved pre-activation
-  const float* act_s;
-  const void* res;            // residual; res_type a DenseType, res_s the scales of an INT8 one
-  const float* res_s;
-  int res_type;
-  int64_t res_ld;             // row pitch of a dense residual, elements
-  void* y;                    // dense output
-  int y_type;
-  int64_t y_ld;
-};
 
 struct GemmArgs {
   int mode;
@@ -125,13 +112,22 @@ struct GemmArgs {
   const float* b_s;
   int64_t rows, cols, depth;  // output rows, output cols, contraction length
   int64_t a_ld, b_ld;         // row pitch (elements) of the stored A and B matrices
-  int8_t* y_q;                // nullable
+  int8_t* y_q;                // nullable: the re-quantized result
   float* y_s;                 // non-null when y_q is
-  float* y_f32;               // nullable
-  int act;                    // GemmAct: activation applied to the fp32 result before y is written
-  int8_t* pre_q;              // nullable (an activated or biased forward only): the re-quantized pre-activation
-  float* pre_s;               // non-null when pre_q is
-  const GemmEpilogue* ep;     // null: the plain epilogue (act kActNone or kActGelu)
+  void* y;                    // nullable: the dense result, y_type a DenseType, y_ld elements per row
+  int y_type;
+  int64_t y_ld;
+  // the linear layers' epilogues (epilogue.cuh); null pointers are absent parts
+  const float* bias;          // forward: fp32 [cols]
+  int act;                    // GemmAct: forward, applied to the result; dgrad, its derivative at act_q / act_s
+  const int8_t* act_q;        // dgrad with an activation: the saved pre-activation
+  const float* act_s;
+  int8_t* pre_q;              // forward: the re-quantized pre-activation
+  float* pre_s;
+  const void* res;            // residual: dense of DenseType res_type, or kResI8 codes with scales res_s
+  const float* res_s;
+  int res_type;
+  int64_t res_ld;             // elements
   unsigned int* status;       // device status word (bit flags of ptx.cuh)
 };
 
