@@ -13,6 +13,7 @@ A quantized tensor is a pair ``QTensor(q, s)``: ``q`` int8 [rows, cols] codes an
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import NamedTuple, Optional
@@ -177,9 +178,17 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr() if t.numel() else None
 
 
-def _stream(stream) -> Optional[int]:
+@functools.lru_cache(None)
+def _has_cuda() -> bool:
+    return torch.cuda.is_available()
+
+
+def _stream(stream, device: int = -1) -> Optional[int]:
+    """The handle of ``stream``, by default the current stream of the device (-1: the current one)."""
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        if not _has_cuda():
+            return None
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device < 0 else device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -374,79 +383,85 @@ def jf_gemm_i8_s32(a: torch.Tensor, b: torch.Tensor, c: torch.Tensor, stream=Non
 
 
 # ---- a transformer block around the linear layer: epilogues, bias gradient, QKV norm and rotation
-class _On:
-    """Makes the device of the tensors of a call current for its duration, after checking that they share one."""
-
-    def __init__(self, *tensors):
-        self.guard = None
-        device = None
-        for t in tensors:
-            for u in (t if isinstance(t, QTensor) else (t,)):
-                if u is None:
-                    continue
-                if device is None:
-                    device = u.device
-                elif u.device != device:
-                    raise ValueError(f"tensors on {device} and {u.device} in one call")
-        if device is None or not torch.cuda.is_available():
-            return   # without a GPU the call refuses by itself
-        if device.type != "cuda":
-            raise ValueError(f"tensors on {device}: the kernels take device memory")
-        if device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _run(where: str, fn, args: tuple, tensors: tuple, stream) -> None:
+    """fn(*args, stream) with the tensors' device current, after checking that they share one. ``tensors``
+    holds tensors, QTensors and Nones."""
+    device = -2
+    for t in tensors:
+        if t is None:
+            continue
+        for u in (t if type(t) is QTensor else (t,)):
+            d = u.get_device()
+            if d != device:
+                if device != -2:
+                    raise ValueError(f"{where}: tensors on different devices ({u.device} among them) in one call")
+                device = d
+    if not _has_cuda():   # the call refuses by itself
+        status = fn(*args, None)
+    elif device < 0:
+        raise ValueError(f"{where}: the kernels take device memory, got CPU tensors")
+    elif device == torch.cuda.current_device():
+        status = fn(*args, _stream(stream, device))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(stream, device))
+    if status != 0:
+        raise JetfireError(status, where)
 
 
-def _q_checked(t: Optional[QTensor], what: str):
-    if t is not None:
-        if t.q.dtype != torch.int8 or t.s.dtype != torch.float32:
-            raise ValueError(f"{what}: codes must be int8 and scales float32")
-        if t.q.dim() != 2 or tuple(t.s.shape) != (t.q.shape[0] // 32, t.q.shape[1] // 32):
-            raise ValueError(f"{what}: scales of shape {tuple(t.s.shape)} do not belong to codes of shape {tuple(t.q.shape)}")
-    return t
+_I8, _F32 = torch.int8, torch.float32
+
+
+def _operand(t: QTensor, what: str, kind=_CQ):
+    """The C struct of a QTensor whose types, shapes and layout have been checked."""
+    q, s = t
+    if q.dtype is not _I8 or s.dtype is not _F32:
+        raise ValueError(f"{what}: codes must be int8 and scales float32")
+    shape = q.shape
+    if len(shape) != 2 or s.shape != (shape[0] // 32, shape[1] // 32):
+        raise ValueError(f"{what}: scales of shape {tuple(s.shape)} do not belong to codes of shape {tuple(shape)}")
+    if not (q.is_contiguous() and s.is_contiguous()):
+        raise ValueError(f"{what}: codes and scales must be contiguous")
+    return kind(q.data_ptr(), s.data_ptr(), shape[0], shape[1])
 
 
 def _f32_vector(t: Optional[torch.Tensor], n: int, what: str) -> Optional[int]:
     if t is None:
         return None
-    if t.dtype != torch.float32 or tuple(t.shape) != (n,):
-        raise ValueError(f"{what} must be float32 of shape ({n},), got {t.dtype} {tuple(t.shape)}")
-    return _ptr(t)
+    if t.dtype is not _F32 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous, float32 and of shape ({n},), got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _matrix(t: Optional[torch.Tensor], rows: int, cols: int, what: str) -> _Matrix:
     """A dense matrix whose rows may be strided (the last dimension is contiguous)."""
     if t is None:
-        return _Matrix(None, 0, cols)
-    if t.dtype not in _DTYPES:
+        return _NO_M
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
         raise ValueError(f"{what}: unsupported dtype {t.dtype}")
-    if tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{what} must have shape ({rows}, {cols}), got {tuple(t.shape)}")
-    if cols > 1 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    return _Matrix(t.data_ptr() if t.numel() else None, _DTYPES[t.dtype], t.stride(0) if rows > 1 else max(cols, 1))
+    return _Matrix(t.data_ptr() if t.numel() else None, dt, ld if rows > 1 else max(cols, 1))
 
 
-_NO_CQ, _NO_Q = _CQ(None, None, 0, 0), _Q(None, None, 0, 0)
+_NO_CQ, _NO_Q, _NO_M = _CQ(None, None, 0, 0), _Q(None, None, 0, 0), _Matrix(None, 0, 0)
 
 
 def _residual(residual, rows: int, cols: int):
-    if isinstance(residual, QTensor):
-        return _cq(_q_checked(residual, "residual")), _matrix(None, rows, cols, "residual")
+    if type(residual) is QTensor:
+        return _operand(residual, "residual"), _NO_M
     return _NO_CQ, _matrix(residual, rows, cols, "residual")
 
 
 def _activation(act: str) -> int:
-    if act not in ACTIVATIONS:
+    code = ACTIVATIONS.get(act)
+    if code is None:
         raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTIVATIONS)}")
-    return ACTIVATIONS[act]
+    return code
 
 
 def jf_linear_fwd_epilogue(X: QTensor, W: QTensor, Y: Optional[QTensor] = None, y: Optional[torch.Tensor] = None,
@@ -456,15 +471,13 @@ def jf_linear_fwd_epilogue(X: QTensor, W: QTensor, Y: Optional[QTensor] = None, 
     strided); P receives the re-quantized pre-activation. The residual is a QTensor or a dense matrix; y
     may be the dense residual itself."""
     lib = load_library()
-    for t, what in ((X, "X"), (W, "W"), (Y, "Y"), (P, "P")):
-        _q_checked(t, what)
-    rows, cols = X.rows, W.rows
+    cx, cw = _operand(X, "X"), _operand(W, "W")
+    rows, cols = cx.rows, cw.rows
     Rq, R = _residual(residual, rows, cols)
-    with _On(X, W, Y, y, bias, residual, P):
-        _check(lib.jf_linear_fwd_epilogue(_cq(X), _cq(W), _f32_vector(bias, cols, "bias"), _activation(act), Rq, R,
-                                          _NO_Q if Y is None else _q(Y, rows, cols), _matrix(y, rows, cols, "y"),
-                                          _NO_Q if P is None else _q(P, rows, cols), _stream(stream)),
-               "jf_linear_fwd_epilogue")
+    _run("jf_linear_fwd_epilogue", lib.jf_linear_fwd_epilogue,
+         (cx, cw, _f32_vector(bias, cols, "bias"), _activation(act), Rq, R, _NO_Q if Y is None else _operand(Y, "Y", _Q),
+          _matrix(y, rows, cols, "y"), _NO_Q if P is None else _operand(P, "P", _Q)),
+         (X, W, Y, y, bias, residual, P), stream)
 
 
 def jf_linear_dgrad_epilogue(dY: QTensor, W: QTensor, dX: Optional[QTensor] = None, dx: Optional[torch.Tensor] = None,
@@ -472,22 +485,20 @@ def jf_linear_dgrad_epilogue(dY: QTensor, W: QTensor, dX: Optional[QTensor] = No
     """Z = (dY W) * act'(pre) + residual into dX (INT8 blocks) and / or dx (dense); pre is the INT8
     pre-activation the forward saved."""
     lib = load_library()
-    for t, what in ((dY, "dY"), (W, "W"), (dX, "dX"), (pre, "pre")):
-        _q_checked(t, what)
-    rows, cols = dY.rows, W.cols
+    cy, cw = _operand(dY, "dY"), _operand(W, "W")
+    rows, cols = cy.rows, cw.cols
     Rq, R = _residual(residual, rows, cols)
-    with _On(dY, W, dX, dx, pre, residual):
-        _check(lib.jf_linear_dgrad_epilogue(_cq(dY), _cq(W), _NO_CQ if pre is None else _cq(pre), _activation(act), Rq, R,
-                                            _NO_Q if dX is None else _q(dX, rows, cols), _matrix(dx, rows, cols, "dx"),
-                                            _stream(stream)), "jf_linear_dgrad_epilogue")
+    _run("jf_linear_dgrad_epilogue", lib.jf_linear_dgrad_epilogue,
+         (cy, cw, _NO_CQ if pre is None else _operand(pre, "pre"), _activation(act), Rq, R,
+          _NO_Q if dX is None else _operand(dX, "dX", _Q), _matrix(dx, rows, cols, "dx")),
+         (dY, W, dX, dx, pre, residual), stream)
 
 
 def jf_bias_grad(dY: QTensor, db: torch.Tensor, stream=None) -> None:
     """db (float32 [cols]) = the column sums of dY."""
     lib = load_library()
-    _q_checked(dY, "dY")
-    with _On(dY, db):
-        _check(lib.jf_bias_grad(_cq(dY), _f32_vector(db, dY.cols, "db"), _stream(stream)), "jf_bias_grad")
+    cy = _operand(dY, "dY")
+    _run("jf_bias_grad", lib.jf_bias_grad, (cy, _f32_vector(db, cy.cols, "db")), (dY, db), stream)
 
 
 def jf_rope_table(inv_freq, cos: torch.Tensor, sin: torch.Tensor, magnitude: float = 1.0, stream=None) -> None:
@@ -498,9 +509,8 @@ def jf_rope_table(inv_freq, cos: torch.Tensor, sin: torch.Tensor, magnitude: flo
         if t.dtype != torch.float32 or t.dim() != 2 or t.shape[1] != half or t.shape != cos.shape:
             raise ValueError(f"{what} must be float32 of shape (length, {half})")
     freq = (ctypes.c_double * max(half, 1))(*[float(f) for f in inv_freq])
-    with _On(cos, sin):
-        _check(lib.jf_rope_table(freq, half, float(magnitude), cos.shape[0], _ptr(cos), _ptr(sin), _stream(stream)),
-               "jf_rope_table")
+    _run("jf_rope_table", lib.jf_rope_table, (freq, half, float(magnitude), cos.shape[0], _ptr(cos), _ptr(sin)), (cos, sin),
+         stream)
 
 
 class QKVRope(NamedTuple):
@@ -523,35 +533,48 @@ class QKVRope(NamedTuple):
 
 
 def _rope(a: QKVRope) -> _Rope:
-    if a.layout not in ROPE_LAYOUTS:
-        raise ValueError(f"unknown layout {a.layout!r}: one of {', '.join(ROPE_LAYOUTS)}")
-    if (a.cos is None) != (a.sin is None):
+    batch, seq, q_heads, kv_heads, d, cos, sin, positions, gamma_q, gamma_k, eps, layout = a
+    code = ROPE_LAYOUTS.get(layout)
+    if code is None:
+        raise ValueError(f"unknown layout {layout!r}: one of {', '.join(ROPE_LAYOUTS)}")
+    if (cos is None) != (sin is None):
         raise ValueError("cos and sin belong together")
     half = length = 0
-    if a.cos is not None:
-        if a.cos.dtype != torch.float32 or a.sin.dtype != torch.float32 or a.cos.dim() != 2 or a.cos.shape != a.sin.shape:
+    pc = ps = None
+    if cos is not None:
+        if cos.dtype is not _F32 or sin.dtype is not _F32 or cos.dim() != 2 or cos.shape != sin.shape:
             raise ValueError("cos and sin must be float32 tables of one shape (length, rot_dim / 2)")
-        length, half = a.cos.shape
-    if a.positions is not None and (a.positions.dtype != torch.int64 or a.positions.numel() != a.batch * a.seq):
-        raise ValueError(f"positions must be int64 with {a.batch * a.seq} elements")
-    return _Rope(a.batch, a.seq, a.q_heads, a.kv_heads, a.head_dim, 2 * half, ROPE_LAYOUTS[a.layout],
-                 None if a.cos is None else _ptr(a.cos), None if a.sin is None else _ptr(a.sin), length,
-                 None if a.positions is None else _ptr(a.positions), _f32_vector(a.gamma_q, a.head_dim, "gamma_q"),
-                 _f32_vector(a.gamma_k, a.head_dim, "gamma_k"), a.eps)
+        length, half = cos.shape
+        pc, ps = _ptr(cos), _ptr(sin)
+    if positions is not None and (positions.dtype is not torch.int64 or positions.numel() != batch * seq):
+        raise ValueError(f"positions must be int64 with {batch * seq} elements")
+    return _Rope(batch, seq, q_heads, kv_heads, d, 2 * half, code, pc, ps, length,
+                 None if positions is None else _ptr(positions), _f32_vector(gamma_q, d, "gamma_q"),
+                 _f32_vector(gamma_k, d, "gamma_k"), eps)
+
+
+_NO_HEADS = _Heads(None, 0, 0, 0)
 
 
 def _heads(t: Optional[torch.Tensor], a: QKVRope, heads: int, heads_first: bool, dtype, what: str) -> _Heads:
     if t is None:
         if heads * a.batch * a.seq:
             raise ValueError(f"{what} is missing")
-        return _Heads(None, 0, 0, 0)
+        return _NO_HEADS
     shape = (a.batch, heads, a.seq, a.head_dim) if heads_first else (a.batch, a.seq, heads, a.head_dim)
-    if t.dtype != dtype or tuple(t.shape) != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what} must be {dtype} of shape {shape}, got {t.dtype} {tuple(t.shape)}")
-    if t.stride(3) != 1 and t.numel():
+    b, x, y, step = t.stride()
+    if step != 1 and t.numel():
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    b, x, y = t.stride(0), t.stride(1), t.stride(2)
-    return _Heads(t.data_ptr() if t.numel() else None, b, y if heads_first else x, x if heads_first else y)
+    return _Heads(t.data_ptr(), b, y, x) if heads_first else _Heads(t.data_ptr(), b, x, y)
+
+
+def _qkv_dtype(*tensors) -> torch.dtype:
+    dtype = next((t.dtype for t in tensors if t is not None), _F32)
+    if dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return dtype
 
 
 def jf_qkv_rope_fwd(qkv: QTensor, a: QKVRope, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
@@ -559,18 +582,15 @@ def jf_qkv_rope_fwd(qkv: QTensor, a: QKVRope, q: Optional[torch.Tensor], k: Opti
     """q, k and v ([batch, seq, heads, head_dim], with heads_first [batch, heads, seq, head_dim]; strided views
     allowed) of the INT8 tensor qkv, queries and keys normed per head and rotated."""
     lib = load_library()
-    _q_checked(qkv, "qkv")
-    given = [t for t in (q, k, v) if t is not None]
-    dtype = given[0].dtype if given else torch.float32
-    if dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {dtype}")
-    t = [_heads(x, a, n, heads_first, dtype, w) for x, n, w in ((q, a.q_heads, "q"), (k, a.kv_heads, "k"), (v, a.kv_heads, "v"))]
-    with _On(qkv, q, k, v, a.cos, a.sin, a.positions, a.gamma_q, a.gamma_k):
-        _check(lib.jf_qkv_rope_fwd(_cq(qkv), ctypes.byref(_rope(a)), *t, _DTYPES[dtype], _stream(stream)), "jf_qkv_rope_fwd")
+    dtype = _qkv_dtype(q, k, v)
+    _run("jf_qkv_rope_fwd", lib.jf_qkv_rope_fwd,
+         (_operand(qkv, "qkv"), _rope(a), _heads(q, a, a.q_heads, heads_first, dtype, "q"),
+          _heads(k, a, a.kv_heads, heads_first, dtype, "k"), _heads(v, a, a.kv_heads, heads_first, dtype, "v"), _DTYPES[dtype]),
+         (qkv, q, k, v, a.cos, a.sin, a.positions, a.gamma_q, a.gamma_k), stream)
 
 
 def jf_qkv_rope_bwd_workspace_bytes(rows: int, a: QKVRope) -> int:
-    return int(load_library().jf_qkv_rope_bwd_workspace_bytes(rows, ctypes.byref(_rope(a))))
+    return int(load_library().jf_qkv_rope_bwd_workspace_bytes(rows, _rope(a)))
 
 
 def jf_qkv_rope_bwd(qkv: QTensor, a: QKVRope, dq, dk, dv, dqkv: QTensor, dgamma_q: Optional[torch.Tensor] = None,
@@ -578,19 +598,14 @@ def jf_qkv_rope_bwd(qkv: QTensor, a: QKVRope, dq, dk, dv, dqkv: QTensor, dgamma_
                     heads_first: bool = False, stream=None) -> None:
     """The gradient of jf_qkv_rope_fwd: dq, dk, dv to INT8 dqkv and the norm weights' gradients."""
     lib = load_library()
-    _q_checked(qkv, "qkv")
-    _q_checked(dqkv, "dqkv")
-    given = [t for t in (dq, dk, dv) if t is not None]
-    dtype = given[0].dtype if given else torch.float32
-    if dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {dtype}")
-    t = [_heads(x, a, n, heads_first, dtype, w) for x, n, w in ((dq, a.q_heads, "dq"), (dk, a.kv_heads, "dk"), (dv, a.kv_heads, "dv"))]
+    dtype = _qkv_dtype(dq, dk, dv)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _On(qkv, dq, dk, dv, dqkv, dgamma_q, dgamma_k, workspace, a.cos, a.sin, a.positions, a.gamma_q, a.gamma_k):
-        _check(lib.jf_qkv_rope_bwd(_cq(qkv), ctypes.byref(_rope(a)), *t, _DTYPES[dtype], _q(dqkv, qkv.rows, qkv.cols),
-                                   _f32_vector(dgamma_q, a.head_dim, "dgamma_q"),
-                                   _f32_vector(dgamma_k, a.head_dim, "dgamma_k"), _ptr(workspace), nbytes,
-                                   _stream(stream)), "jf_qkv_rope_bwd")
+    _run("jf_qkv_rope_bwd", lib.jf_qkv_rope_bwd,
+         (_operand(qkv, "qkv"), _rope(a), _heads(dq, a, a.q_heads, heads_first, dtype, "dq"),
+          _heads(dk, a, a.kv_heads, heads_first, dtype, "dk"), _heads(dv, a, a.kv_heads, heads_first, dtype, "dv"), _DTYPES[dtype],
+          _operand(dqkv, "dqkv", _Q), _f32_vector(dgamma_q, a.head_dim, "dgamma_q"),
+          _f32_vector(dgamma_k, a.head_dim, "dgamma_k"), None if workspace is None else _ptr(workspace), nbytes),
+         (qkv, dq, dk, dv, dqkv, dgamma_q, dgamma_k, workspace, a.cos, a.sin, a.positions, a.gamma_q, a.gamma_k), stream)
 
 
 def jf_selftest_wait_timeout(limit_ns: int, stream=None) -> None:

@@ -30,17 +30,23 @@ namespace jf {
 
 namespace {
 
-// 8 consecutive elements of a dense tensor, to and from fp32.
+// 8 consecutive elements of a dense tensor, loaded and later converted to fp32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    Vec<T>::unpack(ld_stream_v4(p), f);
-  } else {
-    const uint4 a = ld_stream_v4(p), b = ld_stream_v4(p + 4);
-    f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y); f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
-    f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y); f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+struct Raw {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int k = 0; k < int(sizeof(T) / 2); ++k) v[k] = ld_stream_v4(p + 4 * k);
   }
-}
+  __device__ __forceinline__ void unpack(float (&f)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      Vec<T>::unpack(v[0], f);
+    } else {
+      f[0] = __uint_as_float(v[0].x); f[1] = __uint_as_float(v[0].y); f[2] = __uint_as_float(v[0].z); f[3] = __uint_as_float(v[0].w);
+      f[4] = __uint_as_float(v[1].x); f[5] = __uint_as_float(v[1].y); f[6] = __uint_as_float(v[1].z); f[7] = __uint_as_float(v[1].w);
+    }
+  }
+};
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
   if constexpr (sizeof(T) == 2) {
@@ -61,11 +67,6 @@ __device__ __forceinline__ void codes8(const uint2& w, float s, float (&x)[8]) {
   mul_x2(f[2], f[3], s, s, x[6], x[7]);
 }
 
-// What a lane keeps of its token: the rotation's cosines and sines (1 and 0 where it does not rotate).
-struct Angles {
-  float c[8], s[8];
-};
-
 // The two 8-dimension chunks of lane i of a head (in units of 8 columns).
 __device__ __forceinline__ void lane_chunks(int i, int rot, int& c1, int& c2) {
   const int r = rot >> 4;
@@ -73,50 +74,74 @@ __device__ __forceinline__ void lane_chunks(int i, int rot, int& c1, int& c2) {
   c2 = i < r ? i + r : 2 * i + 1;
 }
 
-// Loads the angles of token t for lane i. A position outside the table raises the range bit of *status and
-// makes the angles NaN (fill), or zero in the backward, so that the token's rotated part is NaN (zero).
-__device__ __forceinline__ void load_angles(const QkvRopeArgs& a, int64_t t, int i, float fill, Angles& g) {
+// A rotating lane's 8 cosines and 8 sines: in the half layout pair j of its two chunks turns by c[j], s[j];
+// interleaved, the pairs of its first chunk by c[0..3], those of the second by c[4..7].
+struct Angles {
+  float c[8], s[8];
+  __device__ __forceinline__ void none() {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    g.c[j] = 1.0f;
-    g.s[j] = 0.0f;
+    for (int j = 0; j < 8; ++j) {
+      c[j] = 1.0f;
+      s[j] = 0.0f;
+    }
   }
-  const int r = a.rot >> 4;
-  if (i >= r) return;
-  const int64_t pos = a.positions != nullptr ? __ldg(reinterpret_cast<const long long*>(a.positions) + t) : t % a.seq;
-  if (pos < 0 || pos >= a.table_len) {
-    if (i == 0) atomicOr(a.status, kStatusRange);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) g.c[j] = g.s[j] = fill;
-    return;
+  // From the table row at `row` (elements), its two vectors of four at j0 and j1.
+  __device__ __forceinline__ void load(const QkvRopeArgs& a, int64_t row, int j0, int j1) {
+    const float4 c0 = __ldg(reinterpret_cast<const float4*>(a.cos + row + j0)), c1 = __ldg(reinterpret_cast<const float4*>(a.cos + row + j1));
+    const float4 s0 = __ldg(reinterpret_cast<const float4*>(a.sin + row + j0)), s1 = __ldg(reinterpret_cast<const float4*>(a.sin + row + j1));
+    c[0] = c0.x; c[1] = c0.y; c[2] = c0.z; c[3] = c0.w; c[4] = c1.x; c[5] = c1.y; c[6] = c1.z; c[7] = c1.w;
+    s[0] = s0.x; s[1] = s0.y; s[2] = s0.z; s[3] = s0.w; s[4] = s1.x; s[5] = s1.y; s[6] = s1.z; s[7] = s1.w;
   }
-  // half layout: pairs 8 i .. 8 i + 7; interleaved: chunk i holds pairs 4 i .. 4 i + 3, chunk i + r pairs 4 (i + r) ..
-  const int64_t row = pos * (a.rot >> 1);
-  const int j0 = a.interleaved ? 4 * i : 8 * i, j1 = a.interleaved ? 4 * (i + r) : 8 * i + 4;
-  const float4 c0 = __ldg(reinterpret_cast<const float4*>(a.cos + row + j0)), c1 = __ldg(reinterpret_cast<const float4*>(a.cos + row + j1));
-  const float4 s0 = __ldg(reinterpret_cast<const float4*>(a.sin + row + j0)), s1 = __ldg(reinterpret_cast<const float4*>(a.sin + row + j1));
-  g.c[0] = c0.x; g.c[1] = c0.y; g.c[2] = c0.z; g.c[3] = c0.w; g.c[4] = c1.x; g.c[5] = c1.y; g.c[6] = c1.z; g.c[7] = c1.w;
-  g.s[0] = s0.x; g.s[1] = s0.y; g.s[2] = s0.z; g.s[3] = s0.w; g.s[4] = s1.x; g.s[5] = s1.y; g.s[6] = s1.z; g.s[7] = s1.w;
+};
+
+// Where lane i finds its angles in a table row.
+__device__ __forceinline__ void angle_vectors(const QkvRopeArgs& a, int i, int& j0, int& j1) {
+  j0 = a.interleaved ? 4 * i : 8 * i;
+  j1 = a.interleaved ? 4 * (i + (a.rot >> 4)) : 8 * i + 4;
 }
 
-// Rotates a lane's 16 values by its angles (sign +1) or back (sign -1).
-__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const Angles& g, bool interleaved, float sign) {
-  if (interleaved) {
+// Table row (in elements) of token t, the in_seq-th of its sequence; -1 for a position outside the table,
+// which raises the range bit of *status.
+__device__ __forceinline__ int64_t table_row(const QkvRopeArgs& a, int64_t t, int64_t in_seq, bool report) {
+  const int64_t pos = a.positions != nullptr ? __ldg(reinterpret_cast<const long long*>(a.positions) + t) : in_seq;
+  if (pos < 0 || pos >= a.table_len) {
+    if (report) atomicOr(a.status, kStatusRange);
+    return -1;
+  }
+  return pos * (a.rot >> 1);
+}
+
+// Rotates a lane's 16 values by its angles (forward) or back: packed where the pairs' members are
+// neighbours in registers (half layout), scalar with its free negations for interleaved pairs.
+template <bool BACK, bool INTER>
+__device__ __forceinline__ void rotate(float (&a)[8], float (&b)[8], const Angles& g) {
+  if constexpr (INTER) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float s0 = sign * g.s[j], s1 = sign * g.s[4 + j];
-      const float x0 = a[2 * j], x1 = a[2 * j + 1], z0 = b[2 * j], z1 = b[2 * j + 1];
-      a[2 * j] = fmaf(x0, g.c[j], -(x1 * s0));
-      a[2 * j + 1] = fmaf(x1, g.c[j], x0 * s0);
-      b[2 * j] = fmaf(z0, g.c[4 + j], -(z1 * s1));
-      b[2 * j + 1] = fmaf(z1, g.c[4 + j], z0 * s1);
+    for (int j = 0; j < 8; ++j) {
+      float& x = j < 4 ? a[2 * j] : b[2 * j - 8];
+      float& z = j < 4 ? a[2 * j + 1] : b[2 * j - 7];
+      const float u = BACK ? fmaf(x, g.c[j], z * g.s[j]) : fmaf(x, g.c[j], -(z * g.s[j]));
+      z = BACK ? fmaf(z, g.c[j], -(x * g.s[j])) : fmaf(z, g.c[j], x * g.s[j]);
+      x = u;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float s = sign * g.s[j], x = a[j], z = b[j];
-      a[j] = fmaf(x, g.c[j], -(z * s));
-      b[j] = fmaf(z, g.c[j], x * s);
+    for (int j = 0; j < 8; j += 2) {
+      float p0, p1, q0, q1, r0, r1;
+      mul_x2(b[j], b[j + 1], g.s[j], g.s[j + 1], p0, p1);
+      mul_x2(a[j], a[j + 1], g.s[j], g.s[j + 1], q0, q1);
+      // the difference as product plus -1 times the other product: a packed operand has no sign of its own
+      if (BACK) {
+        fma_x2(a[j], a[j + 1], g.c[j], g.c[j + 1], p0, p1, r0, r1);
+        mul_x2(b[j], b[j + 1], g.c[j], g.c[j + 1], p0, p1);
+        fma_x2(q0, q1, -1.0f, -1.0f, p0, p1, b[j], b[j + 1]);
+      } else {
+        mul_x2(a[j], a[j + 1], g.c[j], g.c[j + 1], r0, r1);
+        fma_x2(p0, p1, -1.0f, -1.0f, r0, r1, r0, r1);
+        fma_x2(b[j], b[j + 1], g.c[j], g.c[j + 1], q0, q1, b[j], b[j + 1]);
+      }
+      a[j] = r0;
+      a[j + 1] = r1;
     }
   }
 }
@@ -137,11 +162,18 @@ __device__ __forceinline__ void load_gamma(const float* gamma, int c1, int c2, f
   g2[0] = c.x; g2[1] = c.y; g2[2] = c.z; g2[3] = c.w; g2[4] = d.x; g2[5] = d.y; g2[6] = d.z; g2[7] = d.w;
 }
 
-// Element offset of (token t, head h) in a dense tensor.
-__device__ __forceinline__ int64_t head_offset(const DenseHeads& d, int64_t t, int64_t seq, int64_t h) {
-  const int64_t b = t / seq;
-  return b * d.stride_b + (t - b * seq) * d.stride_t + h * d.stride_h;
+// a / b for non-negative a and positive b, in 32 bits where both fit (a fifth of the instructions).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
 }
+
+// Sequence b and place s in it of token t.
+__device__ __forceinline__ void token_place(const QkvRopeArgs& a, int64_t t, int64_t& b, int64_t& s) {
+  b = divide(t, a.seq);
+  s = t - b * a.seq;
+}
+// Element offset of that token in a dense tensor.
+__device__ __forceinline__ int64_t token_offset(const DenseHeads& d, int64_t b, int64_t s) { return b * d.stride_b + s * d.stride_t; }
 
 // Sum of squares of 8 codes (exact).
 __device__ __forceinline__ float sumsq8(const uint2& w) { return float(__dp4a(int(w.x), int(w.x), __dp4a(int(w.y), int(w.y), 0))); }
@@ -151,9 +183,10 @@ __device__ __forceinline__ float sumsq8(const uint2& w) { return float(__dp4a(in
 // and a range of the heads (blockIdx.y).
 // ---------------------------------------------------------------------------------------------
 constexpr int kFwdWarps = 4;
+constexpr int kAhead = 4;
 
-template <typename T, int G>
-__global__ void __launch_bounds__(32 * kFwdWarps) qkv_rope_fwd_kernel(const QkvRopeArgs a, int heads_per_warp) {
+template <typename T, int G, bool INTER>
+__global__ void __launch_bounds__(32 * kFwdWarps, 5) qkv_rope_fwd_kernel(const QkvRopeArgs a, int heads_per_warp) {
   const int lane = threadIdx.x & 31, i = lane % G, n = a.d >> 4;
   const int64_t t = (int64_t(blockIdx.x) * kFwdWarps + (threadIdx.x >> 5)) * (32 / G) + lane / G;
   const bool live = i < n && t < a.tokens;
@@ -162,137 +195,271 @@ __global__ void __launch_bounds__(32 * kFwdWarps) qkv_rope_fwd_kernel(const QkvR
   int c1, c2;
   lane_chunks(i, a.rot, c1, c2);
   Angles ang;
-  if (live && h0 < a.hq + a.hkv) load_angles(a, t, i, __int_as_float(0x7FC00000), ang);
-  const int64_t nbc = a.cols >> 5;
-  const int8_t* row = a.x_q + t * a.cols;
-  const float* srow = a.x_s + (t >> 5) * nbc;
-  float g1[8], g2[8];
-  const float* gamma = nullptr;
-  for (int h = h0; h < h1; ++h) {
-    const int kind = h < a.hq ? 0 : h < a.hq + a.hkv ? 1 : 2;
-    const float* gm = kind == 0 ? a.gamma_q : kind == 1 ? a.gamma_k : nullptr;
-    if (gm != gamma) {
-      if (gm != nullptr && i < n) load_gamma(gm, c1, c2, g1, g2);
-      gamma = gm;
-    }
-    uint2 w1 = make_uint2(0u, 0u), w2 = w1;
-    float s1 = 0.0f, s2 = 0.0f;
-    const int64_t col = int64_t(h) * a.d;
-    if (live) {
-      w1 = ld_stream_v2(row + col + 8 * c1);
-      w2 = ld_stream_v2(row + col + 8 * c2);
-      s1 = __ldg(srow + ((col + 8 * c1) >> 5));
-      s2 = __ldg(srow + ((col + 8 * c2) >> 5));
-    }
-    float x1[8], x2[8];
-    if (gm != nullptr) {
-      const float ss = head_sum<G>(fmaf(s1 * s1, sumsq8(w1), s2 * s2 * sumsq8(w2)));
-      const float r = 1.0f / sqrtf(ss / float(a.d) + a.eps);
-      codes8(w1, s1 * r, x1);
-      codes8(w2, s2 * r, x2);
+  int64_t bt = 0, st = 0;
+  if (live) {
+    token_place(a, t, bt, st);
+    ang.none();
+    if (h0 < a.hq + a.hkv && i < (a.rot >> 4)) {
+      const int64_t row = table_row(a, t, st, i == 0);
+      int j0, j1;
+      angle_vectors(a, i, j0, j1);
+      if (row >= 0) {
+        ang.load(a, row, j0, j1);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x1[j] *= g1[j];
-        x2[j] *= g2[j];
+        for (int j = 0; j < 8; ++j) ang.c[j] = ang.s[j] = __int_as_float(0x7FC00000);   // NaN
       }
-    } else {
-      codes8(w1, s1, x1);
-      codes8(w2, s2, x2);
     }
-    if (!live) continue;
-    if (kind < 2) rotate(x1, x2, ang, a.interleaved, 1.0f);
+  }
+  const float inv_d = 1.0f / float(a.d);
+  const int8_t* row = a.x_q + t * a.cols;
+  const float* srow = a.x_s + (t >> 5) * (a.cols >> 5);
+  // One kind of head at a time; the codes of kAhead heads are loaded together, before the first is used.
+  for (int kind = 0; kind < 3; ++kind) {
+    const int base = kind == 0 ? 0 : kind == 1 ? a.hq : a.hq + a.hkv, num = kind == 0 ? a.hq : a.hkv;
+    const int lo = max(h0, base), hi = min(h1, base + num);
+    if (lo >= hi) continue;
+    const float* gamma = kind == 0 ? a.gamma_q : kind == 1 ? a.gamma_k : nullptr;
+    float g1[8], g2[8];
+    if (gamma != nullptr && i < n) load_gamma(gamma, c1, c2, g1, g2);
     const DenseHeads& d = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-    const int hh = kind == 0 ? h : kind == 1 ? h - a.hq : h - a.hq - a.hkv;
-    T* out = static_cast<T*>(d.p) + head_offset(d, t, a.seq, hh);
-    store8(out + 8 * c1, x1);
-    store8(out + 8 * c2, x2);
+    T* out = static_cast<T*>(d.p) + token_offset(d, bt, st) - base * d.stride_h;
+    for (int hb = lo; hb < hi; hb += kAhead) {
+      uint2 w1[kAhead], w2[kAhead];
+      float s1[kAhead], s2[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        w1[u] = w2[u] = make_uint2(0u, 0u);
+        s1[u] = s2[u] = 0.0f;
+        if (live && hb + u < hi) {
+          const int64_t col = int64_t(hb + u) * a.d;
+          w1[u] = ld_stream_v2(row + col + 8 * c1);
+          w2[u] = ld_stream_v2(row + col + 8 * c2);
+          s1[u] = __ldg(srow + ((col + 8 * c1) >> 5));
+          s2[u] = __ldg(srow + ((col + 8 * c2) >> 5));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (hb + u >= hi) break;
+        float x1[8], x2[8];
+        if (gamma != nullptr) {
+          const float ss = head_sum<G>(fmaf(s1[u] * s1[u], sumsq8(w1[u]), s2[u] * s2[u] * sumsq8(w2[u])));
+          const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+          codes8(w1[u], s1[u] * r, x1);
+          codes8(w2[u], s2[u] * r, x2);
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            mul_x2(x1[j], x1[j + 1], g1[j], g1[j + 1], x1[j], x1[j + 1]);
+            mul_x2(x2[j], x2[j + 1], g2[j], g2[j + 1], x2[j], x2[j + 1]);
+          }
+        } else {
+          codes8(w1[u], s1[u], x1);
+          codes8(w2[u], s2[u], x2);
+        }
+        if (!live) continue;
+        if (kind < 2) rotate<false, INTER>(x1, x2, ang);
+        T* o = out + (hb + u) * d.stride_h;
+        store8(o + 8 * c1, x1);
+        store8(o + 8 * c2, x2);
+      }
+    }
   }
 }
 
 // ---------------------------------------------------------------------------------------------
 // Backward: reads dq, dk, dv, and with a norm the codes of the queries and keys; writes INT8. The G warps of a
 // slot hold one head of a 32-token strip at a time, 16 values a lane; a block's absmax goes through
-// shared memory (integer maxima of the bit patterns: their order does not matter). Persistent CTAs take
-// work items (strip, run of heads of one kind) in turn; the weights' gradients stay in registers while the
-// kind lasts and are then added into the CTA's row of the workspace; a second kernel adds the rows in a
-// fixed order in fp64.
+// shared memory (integer maxima of the bit patterns: their order does not matter). A lane copies what it
+// will need of the next heads into its own places of a shared-memory ring (cp.async), so that loads in
+// flight take no registers. The slots of a persistent grid share the strips and heads of one kind evenly,
+// each a contiguous range; the weights' gradients stay in registers while the kind lasts and are then added
+// into the CTA's row of the workspace; a second kernel adds the rows in a fixed order in fp64.
 // ---------------------------------------------------------------------------------------------
 constexpr int kBwdWarps = 8;
 
-template <typename T, int G>
-__global__ void __launch_bounds__(32 * (G > kBwdWarps ? G : kBwdWarps)) qkv_rope_bwd_kernel(const QkvRopeArgs a, int heads_per_item) {
+// Codes of two values in a block with a normal scale: tp = x inv + kRoundMagic rounds x inv to an integer, and
+// far keeps the largest distance from it. inv is within 1 ulp of 1 / s, so x inv is within 127 x 2^-23 < 2^-16 of
+// x / s, whose IEEE quotient is within 2^-18 of it: farther than 2^-15 from every tie both round alike
+// (quant_byte's argument with one rounding less, hence half its window).
+__device__ __forceinline__ void code_pair(float x0, float x1, float inv, uint32_t& c0, uint32_t& c1, float& far) {
+  float t0, t1, r0, r1, d0, d1;
+  fma_x2(x0, x1, inv, inv, kRoundMagic, kRoundMagic, t0, t1);
+  fma_x2(t0, t1, -1.0f, -1.0f, kRoundMagic, kRoundMagic, r0, r1);   // minus the integer, exact
+  fma_x2(x0, x1, inv, inv, r0, r1, d0, d1);
+  asm("max.f32 %0, %0, %1, %2;" : "+f"(far) : "f"(fabsf(d0)), "f"(fabsf(d1)));
+  c0 = __float_as_uint(t0);
+  c1 = __float_as_uint(t1);
+}
+
+// Codes of a lane's two chunks with the reciprocals of their blocks' scales: one test for values next to a
+// rounding tie for all 16 (false: a few percent of the warps), after which quant_pack decides.
+__device__ __forceinline__ bool codes16(const float (&y1)[8], const float (&y2)[8], float inv1, float inv2, uint2& w1, uint2& w2) {
+  uint32_t c[8], e[8];
+  float far = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    code_pair(y1[j], y1[j + 1], inv1, c[j], c[j + 1], far);
+    code_pair(y2[j], y2[j + 1], inv2, e[j], e[j + 1], far);
+  }
+  w1 = make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
+  w2 = make_uint2(pack4(e[0], e[1], e[2], e[3]), pack4(e[4], e[5], e[6], e[7]));
+  return far < 0.499969482421875f;   // 0.5 - 2^-15
+}
+
+constexpr int kRing = 3;   // heads of the ring: two on their way while one is at work
+
+// A lane's places in the ring: 16-byte pieces of the gradient's two chunks, then 8 bytes of codes of each.
+template <typename T, int THREADS>
+struct Ring {
+  static constexpr int kPieces = int(sizeof(T)) / 2;                     // 16-byte pieces of 8 elements
+  static constexpr int kHead = THREADS * (2 * kPieces * 16 + 16);        // bytes of one head's data
+  static constexpr int kBytes = kRing * kHead;
+};
+
+template <typename T, int G, bool INTER>
+__global__ void __launch_bounds__(32 * (G > kBwdWarps ? G : kBwdWarps), G > kBwdWarps ? 1 : 2) qkv_rope_bwd_kernel(const QkvRopeArgs a) {
   constexpr int W = G > kBwdWarps ? G : kBwdWarps;
-  constexpr int SLOTS = W / G;          // heads in flight
+  constexpr int SLOTS = W / G;              // heads in flight
+  using R = Ring<T, 32 * W>;
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ uint32_t s_max[3][SLOTS][8];
-  __shared__ float s_part[W][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = warp / G;
-  const int i = lane % G, n = a.d >> 4;
+  const int i = lane % G, n = a.d >> 4, nblk = a.d >> 5;
   const int tl = (warp % G) * (32 / G) + lane / G;   // token in the strip
-  int c1, c2;
+  int c1, c2, j0, j1;
   lane_chunks(i, a.rot, c1, c2);
+  angle_vectors(a, i, j0, j1);
+  // shared-memory addresses of the lane's pieces (at stride 16 x threads) and codes in ring place 0
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
+  const uint32_t mine_w = smem_u32(ring) + 32 * W * 2 * R::kPieces * 16 + threadIdx.x * 8;
   const int64_t nbc = a.cols >> 5, strips = a.rows >> 5;
   if (threadIdx.x < 3 * SLOTS * 8) (&s_max[0][0][0])[threadIdx.x] = 0u;
   __syncthreads();
-  int it = 0;                            // this slot's blocks so far: s_max[it % 3] is in use
+  const float inv_d = 1.0f / float(a.d);
+  int it = 0;                            // this slot's blocks so far: s_max[it] (modulo 3) is in use
   for (int kind = 0; kind < 3; ++kind) {
     const int heads = kind == 0 ? a.hq : a.hkv;
     const int base = kind == 0 ? 0 : kind == 1 ? a.hq : a.hq + a.hkv;
     const DenseHeads& d = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
     const float* gamma = kind == 0 ? a.gamma_q : kind == 1 ? a.gamma_k : nullptr;
-    float g1[8], g2[8], dg1[8], dg2[8];
+    float dg1[8], dg2[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg1[j] = dg2[j] = 0.0f;
+    float g1[8], g2[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g1[j] = g2[j] = 0.0f;
     if (gamma != nullptr && i < n) load_gamma(gamma, c1, c2, g1, g2);
-    const int runs = (heads + heads_per_item - 1) / heads_per_item;
-    for (int64_t item = blockIdx.x; item < strips * runs; item += gridDim.x) {
-      const int64_t strip = item / runs;
-      const int h0 = int(item - strip * runs) * heads_per_item, h1 = min(h0 + heads_per_item, heads);
+    // the slots share the strips x heads of this kind evenly, each a contiguous range (strip by strip)
+    const int64_t units = strips * heads, slots = int64_t(gridDim.x) * SLOTS, me = int64_t(blockIdx.x) * SLOTS + slot;
+    const int64_t share = divide(units, slots), more = units - share * slots;
+    const int64_t u0 = me * share + min(me, more);
+    int64_t left = heads > 0 ? share + (me < more ? 1 : 0) : 0;
+    int64_t strip = heads > 0 ? divide(u0, heads) : 0;
+    int h0 = int(u0 - strip * heads);
+    for (; left > 0; ++strip, h0 = 0) {
+      const int h1 = int(min(int64_t(heads), h0 + left));
+      left -= h1 - h0;
       const int64_t t = strip * 32 + tl;
       const bool live = i < n && t < a.tokens;
+      const bool turns = kind < 2 && live && i < (a.rot >> 4);
+      int64_t bt = 0, st = 0;
+      if (live) token_place(a, t, bt, st);
       Angles ang;
-      if (live && kind < 2) load_angles(a, t, i, 0.0f, ang);
-      for (int h = h0 + slot; h < h1; h += SLOTS, ++it) {
-        const int64_t col = int64_t(base + h) * a.d;
-        const int64_t b1 = (col + 8 * c1) >> 5, b2 = (col + 8 * c2) >> 5;
-        float y1[8], y2[8];
+      ang.none();
+      if (turns) {
+        const int64_t row = table_row(a, t, st, i == 0);
+        if (row >= 0) {
+          ang.load(a, row, j0, j1);
+        } else {   // a position outside the table: no gradient
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y1[j] = y2[j] = 0.0f;
-        uint2 w1 = make_uint2(0u, 0u), w2 = w1;
-        float s1 = 0.0f, s2 = 0.0f;
-        if (live) {
-          const T* src = static_cast<const T*>(d.p) + head_offset(d, t, a.seq, h);
-          load8(src + 8 * c1, y1);
-          load8(src + 8 * c2, y2);
-          if (gamma != nullptr) {
-            w1 = ld_stream_v2(a.x_q + t * a.cols + col + 8 * c1);
-            w2 = ld_stream_v2(a.x_q + t * a.cols + col + 8 * c2);
-            s1 = __ldg(a.x_s + strip * nbc + b1);
-            s2 = __ldg(a.x_s + strip * nbc + b2);
-          }
-          if (kind < 2) rotate(y1, y2, ang, a.interleaved, -1.0f);
+          for (int j = 0; j < 8; ++j) ang.c[j] = ang.s[j] = 0.0f;
+        }
+      }
+      // a lane without a token copies nothing (from an address that is valid all the same) and gets zeros,
+      // from which everything below is zero
+      const T* src = live ? static_cast<const T*>(d.p) + token_offset(d, bt, st) + h0 * d.stride_h + 8 * c1
+                          : reinterpret_cast<const T*>(a.dx_q);
+      const int8_t* xr = live ? a.x_q + t * a.cols + int64_t(base + h0) * a.d + 8 * c1 : a.dx_q;
+      const int64_t step_s = live ? d.stride_h : 0, step_x = live ? a.d : 0;
+      const int next_s = live ? 8 * (c2 - c1) : 0;
+      int8_t* dst = a.dx_q + t * a.cols + int64_t(base + h0) * a.d + 8 * c1;
+      int64_t blk = strip * nbc + ((int64_t(base + h0) * a.d) >> 5);   // the head's first block
+      const uint32_t take16 = live ? 16u : 0u, take8 = live ? 8u : 0u;
+      uint32_t put = 0;                  // byte offset of the ring place to fill next
+      auto fetch = [&]() {               // the next head in turn
+        const T* src2 = src + next_s;
+#pragma unroll
+        for (int k = 0; k < R::kPieces; ++k) {
+          cp_async_16(mine + put + k * (32 * W * 16), reinterpret_cast<const uint4*>(src) + k, take16);
+          cp_async_16(mine + put + (R::kPieces + k) * (32 * W * 16), reinterpret_cast<const uint4*>(src2) + k, take16);
         }
         if (gamma != nullptr) {
+          cp_async_8(mine_w + put, xr, take8);
+          cp_async_8(mine_w + put + 32 * W * 8, xr + next_s, take8);
+        }
+        src += step_s;
+        xr += step_x;
+        put = put == (kRing - 1) * R::kHead ? 0 : put + R::kHead;
+      };
+#pragma unroll
+      for (int k = 0; k < kRing - 1; ++k) {
+        if (h0 + k < h1) fetch();
+        cp_async_commit();
+      }
+      uint32_t get = 0;                  // ring place of the head at work
+      float s1n = 0.0f, s2n = 0.0f;      // the next head's scales
+      auto scales = [&](int64_t b) {
+        if (gamma != nullptr && live) {
+          s1n = __ldg(a.x_s + b + (c1 >> 2));
+          s2n = __ldg(a.x_s + b + (c2 >> 2));
+        }
+      };
+      if (h0 < h1) scales(blk);
+      for (int h = h0; h < h1; ++h) {
+        cp_async_wait<kRing - 2>();      // this lane's own copies: no barrier
+        float y1[8], y2[8];
+        uint2 w1 = make_uint2(0u, 0u), w2 = w1;
+        const float s1 = s1n, s2 = s2n;
+        Raw<T> r1, r2;
+#pragma unroll
+        for (int k = 0; k < R::kPieces; ++k) {
+          r1.v[k] = lds_v4(mine + get + k * (32 * W * 16));
+          r2.v[k] = lds_v4(mine + get + (R::kPieces + k) * (32 * W * 16));
+        }
+        if (gamma != nullptr) {
+          w1 = lds_v2(mine_w + get);
+          w2 = lds_v2(mine_w + get + 32 * W * 8);
+        }
+        r1.unpack(y1);
+        r2.unpack(y2);
+        if (h + kRing - 1 < h1) fetch();
+        cp_async_commit();
+        get = get == (kRing - 1) * R::kHead ? 0 : get + R::kHead;
+        if (h + 1 < h1) scales(blk + (a.d >> 5));
+        if (kind < 2) rotate<true, INTER>(y1, y2, ang);
+        if (gamma != nullptr) {
           const float ss = head_sum<G>(fmaf(s1 * s1, sumsq8(w1), s2 * s2 * sumsq8(w2)));
-          const float r = 1.0f / sqrtf(ss / float(a.d) + a.eps);
-          float x1[8], x2[8], m = 0.0f;   // xhat, and the sum of g xhat
+          const float r = rsqrtf(fmaf(ss, inv_d, a.eps));   // eps > 0: finite, and a head that is not there stays 0
+          float x1[8], x2[8], m0 = 0.0f, m1 = 0.0f;         // xhat, and the sum of g xhat
           codes8(w1, s1 * r, x1);
           codes8(w2, s2 * r, x2);
-          if (live) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              dg1[j] = fmaf(y1[j], x1[j], dg1[j]);
-              dg2[j] = fmaf(y2[j], x2[j], dg2[j]);
-              y1[j] *= g1[j];
-              y2[j] *= g2[j];
-              m = fmaf(y1[j], x1[j], m);
-              m = fmaf(y2[j], x2[j], m);
-            }
+          for (int j = 0; j < 8; j += 2) {
+            fma_x2(y1[j], y1[j + 1], x1[j], x1[j + 1], dg1[j], dg1[j + 1], dg1[j], dg1[j + 1]);
+            fma_x2(y2[j], y2[j + 1], x2[j], x2[j + 1], dg2[j], dg2[j + 1], dg2[j], dg2[j + 1]);
+            mul_x2(y1[j], y1[j + 1], g1[j], g1[j + 1], y1[j], y1[j + 1]);
+            mul_x2(y2[j], y2[j + 1], g2[j], g2[j + 1], y2[j], y2[j + 1]);
+            fma_x2(y1[j], y1[j + 1], x1[j], x1[j + 1], m0, m1, m0, m1);
+            fma_x2(y2[j], y2[j + 1], x2[j], x2[j + 1], m0, m1, m0, m1);
           }
-          m = head_sum<G>(m) / float(a.d);   // eps > 0 keeps r finite: a head that is not there stays 0
+          const float m = -(head_sum<G>(m0 + m1) * inv_d);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            y1[j] = r * fmaf(-x1[j], m, y1[j]);
-            y2[j] = r * fmaf(-x2[j], m, y2[j]);
+          for (int j = 0; j < 8; j += 2) {
+            fma_x2(x1[j], x1[j + 1], m, m, y1[j], y1[j + 1], y1[j], y1[j + 1]);
+            fma_x2(x2[j], x2[j + 1], m, m, y2[j], y2[j + 1], y2[j], y2[j + 1]);
+            mul_x2(y1[j], y1[j + 1], r, r, y1[j], y1[j + 1]);
+            mul_x2(y2[j], y2[j + 1], r, r, y2[j], y2[j + 1]);
           }
         }
         // absmax of the head's D / 32 blocks over the strip's 32 tokens
@@ -307,28 +474,36 @@ __global__ void __launch_bounds__(32 * (G > kBwdWarps ? G : kBwdWarps)) qkv_rope
           m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
           m2 = fmaxf(m2, __shfl_xor_sync(0xffffffffu, m2, o));
         }
-        uint32_t* mx = s_max[it % 3][slot];
+        uint32_t* mx = s_max[it][slot];
         if (lane < G && i < n) {
           atomicMax(mx + (c1 >> 2), __float_as_uint(m1));
           atomicMax(mx + (c2 >> 2), __float_as_uint(m2));
         }
         named_bar_sync(1 + slot, 32 * G);
         // the buffer of the block before this one is free now: every warp has read it before this barrier
-        if (warp % G == 0 && lane < 8) s_max[(it + 2) % 3][slot][lane] = 0u;
-        if (i < n) {
-          const BlockQuant q1 = block_quant(__uint_as_float(mx[c1 >> 2])), q2 = block_quant(__uint_as_float(mx[c2 >> 2]));
-          uint32_t o1[2], o2[2];
-          quant_pack<8>(y1, q1, o1);
-          quant_pack<8>(y2, q2, o2);
-          int8_t* dst = a.dx_q + t * a.cols + col;
-          *reinterpret_cast<uint2*>(dst + 8 * c1) = make_uint2(o1[0], o1[1]);
-          *reinterpret_cast<uint2*>(dst + 8 * c2) = make_uint2(o2[0], o2[1]);
-          if (tl == 0) {
-            if ((c1 & 3) == 0) a.dx_s[strip * nbc + b1] = q1.s;
-            if ((c2 & 3) == 0) a.dx_s[strip * nbc + b2] = q2.s;
-          }
+        if (warp % G == 0 && lane < 8) s_max[it == 0 ? 2 : it - 1][slot][lane] = 0u;
+        it = it == 2 ? 0 : it + 1;
+        // lane l computes block l % 8's scale; the others fetch their two blocks' reciprocals from there
+        const BlockQuant bq = block_quant_approx(__uint_as_float(mx[lane & 7]));
+        const float inv1 = __shfl_sync(0xffffffffu, bq.inv, c1 >> 2), inv2 = __shfl_sync(0xffffffffu, bq.inv, c2 >> 2);
+        const bool plain = __all_sync(0xffffffffu, bq.mode == 2 || (lane & 7) >= nblk);   // normal scales only
+        uint2 o1, o2;
+        if (!codes16(y1, y2, inv1, inv2, o1, o2) || !plain) {
+          uint32_t w[2];
+          quant_pack<8>(y1, block_quant_approx(__uint_as_float(mx[c1 >> 2])), w);
+          o1 = make_uint2(w[0], w[1]);
+          quant_pack<8>(y2, block_quant_approx(__uint_as_float(mx[c2 >> 2])), w);
+          o2 = make_uint2(w[0], w[1]);
         }
+        if (i < n) {
+          *reinterpret_cast<uint2*>(dst) = o1;
+          *reinterpret_cast<uint2*>(dst + 8 * (c2 - c1)) = o2;
+        }
+        if (warp % G == 0 && lane < nblk) a.dx_s[blk + lane] = bq.s;
+        dst += a.d;
+        blk += a.d >> 5;
       }
+      cp_async_wait<0>();                // the next strip starts with an empty ring
     }
     if (gamma != nullptr && a.part != nullptr) {
       // this CTA's sums: over a warp's tokens by shuffles, then over the warps in order
@@ -340,21 +515,23 @@ __global__ void __launch_bounds__(32 * (G > kBwdWarps ? G : kBwdWarps)) qkv_rope
           dg2[j] += __shfl_xor_sync(0xffffffffu, dg2[j], o);
         }
       }
-      __syncthreads();                   // the previous kind's sums have been read
+      float* s_part = reinterpret_cast<float*>(ring);   // [W][256]: the ring is empty between kinds
+      __syncthreads();                   // the previous kind's sums have been read, every warp's copies are used
       if (lane < G && i < n) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          s_part[warp][8 * c1 + j] = dg1[j];
-          s_part[warp][8 * c2 + j] = dg2[j];
+          s_part[warp * 256 + 8 * c1 + j] = dg1[j];
+          s_part[warp * 256 + 8 * c2 + j] = dg2[j];
         }
       }
       __syncthreads();
       for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) sum += s_part[w][c];
+        for (int w = 0; w < W; ++w) sum += s_part[w * 256 + c];
         a.part[(int64_t(blockIdx.x) * 2 + kind) * a.d + c] = sum;
       }
+      __syncthreads();                   // before the ring is filled again
     }
   }
 }
@@ -397,7 +574,7 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__
 
 int group_of(int64_t d) { return d <= 32 ? 2 : d <= 64 ? 4 : d <= 128 ? 8 : 16; }
 
-template <typename T, int G>
+template <typename T, int G, bool INTER>
 cudaError_t fwd(const QkvRopeArgs& a, int sm_count, cudaStream_t st) {
   const int heads = a.hq + 2 * a.hkv;
   const int64_t gx = (a.tokens + kFwdWarps * (32 / G) - 1) / (kFwdWarps * (32 / G));
@@ -407,40 +584,54 @@ cudaError_t fwd(const QkvRopeArgs& a, int sm_count, cudaStream_t st) {
   per = per < 1 ? 1 : per > heads ? heads : per;
   const int64_t gy = (heads + per - 1) / per;
   if (gy > 65535 || gx > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  qkv_rope_fwd_kernel<T, G><<<dim3(unsigned(gx), unsigned(gy)), 32 * kFwdWarps, 0, st>>>(a, int(per));
+  qkv_rope_fwd_kernel<T, G, INTER><<<dim3(unsigned(gx), unsigned(gy)), 32 * kFwdWarps, 0, st>>>(a, int(per));
   return cudaGetLastError();
 }
 
-template <typename T, int G>
+template <typename T, int G, bool INTER>
 cudaError_t bwd(const QkvRopeArgs& a, int sm_count, cudaStream_t st) {
-  constexpr int W = G > kBwdWarps ? G : kBwdWarps, SLOTS = W / G;
-  const int64_t strips = a.rows / 32, ctas = qkv_bwd_ctas(a.rows, a.hq, a.hkv);
-  // runs of heads long enough to reuse a strip's angles, short enough for several items per CTA
-  int64_t per = strips * a.hq / (ctas * 4);
-  per = per < SLOTS ? SLOTS : per > 8 ? 8 : per;
-  qkv_rope_bwd_kernel<T, G><<<unsigned(ctas), 32 * W, 0, st>>>(a, int(per));
-  cudaError_t e = cudaGetLastError();
+  constexpr int W = G > kBwdWarps ? G : kBwdWarps;
+  constexpr int smem = Ring<T, 32 * W>::kBytes;
+  static_assert(smem >= W * 256 * 4, "the warps' column sums fit in the ring");
+  static unsigned long long attr_set = 0;   // one bit per device ordinal
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024 && !(attr_set >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(qkv_rope_bwd_kernel<T, G, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    attr_set |= 1ull << (dev & 63);
+  }
+  const int64_t ctas = qkv_bwd_ctas(a.rows, a.hq, a.hkv);
+  qkv_rope_bwd_kernel<T, G, INTER><<<unsigned(ctas), 32 * W, smem, st>>>(a);
+  e = cudaGetLastError();
   if (e != cudaSuccess || a.part == nullptr) return e;
   qkv_dgamma_kernel<<<dim3(unsigned(a.d / 32), 2), 256, 0, st>>>(a.part, int(ctas), a.d, a.dgamma_q, a.dgamma_k);
   return cudaGetLastError();
 }
 
-template <typename T>
+template <typename T, bool INTER>
 cudaError_t run(const QkvRopeArgs& a, bool backward, int sm_count, cudaStream_t st) {
   switch (group_of(a.d)) {
-    case 2: return backward ? bwd<T, 2>(a, sm_count, st) : fwd<T, 2>(a, sm_count, st);
-    case 4: return backward ? bwd<T, 4>(a, sm_count, st) : fwd<T, 4>(a, sm_count, st);
-    case 8: return backward ? bwd<T, 8>(a, sm_count, st) : fwd<T, 8>(a, sm_count, st);
-    default: return backward ? bwd<T, 16>(a, sm_count, st) : fwd<T, 16>(a, sm_count, st);
+    case 2: return backward ? bwd<T, 2, INTER>(a, sm_count, st) : fwd<T, 2, INTER>(a, sm_count, st);
+    case 4: return backward ? bwd<T, 4, INTER>(a, sm_count, st) : fwd<T, 4, INTER>(a, sm_count, st);
+    case 8: return backward ? bwd<T, 8, INTER>(a, sm_count, st) : fwd<T, 8, INTER>(a, sm_count, st);
+    default: return backward ? bwd<T, 16, INTER>(a, sm_count, st) : fwd<T, 16, INTER>(a, sm_count, st);
   }
+}
+
+template <typename T>
+cudaError_t run(const QkvRopeArgs& a, bool backward, int sm_count, cudaStream_t st) {
+  return a.interleaved ? run<T, true>(a, backward, sm_count, st) : run<T, false>(a, backward, sm_count, st);
 }
 
 }  // namespace
 
 // CTAs of the backward: at most two for each of 148 SMs, at most one per strip and head.
+constexpr int64_t kQkvBwdMaxCtas = 296;
 int64_t qkv_bwd_ctas(int64_t rows, int64_t hq, int64_t hkv) {
   const int64_t work = rows / 32 * (hq + 2 * hkv);
-  return work < 296 ? (work < 1 ? 1 : work) : 296;
+  return work < kQkvBwdMaxCtas ? (work < 1 ? 1 : work) : kQkvBwdMaxCtas;
 }
 
 cudaError_t launch_qkv_rope(const QkvRopeArgs& a, bool backward, int dtype, int sm_count, cudaStream_t st) {

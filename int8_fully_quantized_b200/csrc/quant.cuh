@@ -31,6 +31,17 @@ __device__ __forceinline__ BlockQuant block_quant(float amax) {
   return b;
 }
 
+// block_quant with the hardware's approximate reciprocal (1 ulp) of a normal scale. The codes stay exact: with
+// |x/s| <= 127 (1 + 2^-23), |t - x/s| <= 127 (2^-23 + 2^-24) < 2^-15.4 and the IEEE quotient is within 2^-18 of
+// x/s, so t is within 2^-15 of it, the distance quant_byte's fast path is proven for.
+__device__ __forceinline__ BlockQuant block_quant_approx(float amax) {
+  BlockQuant b;
+  b.s = __fdiv_rn(amax, kQMax);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(b.inv) : "f"(b.s));   // s <= 2^128 / 127: the reciprocal is normal
+  b.mode = (b.s == 0.0f) ? 0 : (b.s < kFltMinNormal ? 1 : 2);
+  return b;
+}
+
 // Exact path of quant_byte: the IEEE quotient, clamped, rounded half to even (kept out of line so
 // that the unrolled callers stay small; it runs only for values next to a rounding tie or for
 // blocks with a subnormal scale).
