@@ -383,30 +383,32 @@ def jf_gemm_i8_s32(a: torch.Tensor, b: torch.Tensor, c: torch.Tensor, stream=Non
 
 
 # ---- a transformer block around the linear layer: epilogues, bias gradient, QKV norm and rotation
-def _run(where: str, fn, args: tuple, tensors: tuple, stream) -> None:
-    """fn(*args, stream) with the tensors' device current, after checking that they share one. ``tensors``
-    holds tensors, QTensors and Nones."""
-    device = -2
-    for t in tensors:
-        if t is None:
-            continue
-        for u in (t if type(t) is QTensor else (t,)):
-            d = u.get_device()
-            if d != device:
-                if device != -2:
-                    raise ValueError(f"{where}: tensors on different devices ({u.device} among them) in one call")
-                device = d
+def _device(where: str, first: torch.Tensor, *rest: Optional[torch.Tensor]) -> int:
+    """The device index that all the tensors (Nones apart) share; -1 for host memory."""
+    d = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != d:
+            raise ValueError(f"{where}: tensors on {first.device} and {t.device} in one call")
+    return d
+
+
+def _run(where: str, fn, args: tuple, device: int, stream) -> None:
+    """fn(*args, stream) with the tensors' device current."""
     if not _has_cuda():   # the call refuses by itself
         status = fn(*args, None)
     elif device < 0:
         raise ValueError(f"{where}: the kernels take device memory, got CPU tensors")
     elif device == torch.cuda.current_device():
-        status = fn(*args, _stream(stream, device))
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(device):
             status = fn(*args, _stream(stream, device))
     if status != 0:
         raise JetfireError(status, where)
+
+
+def _parts(t) -> tuple:
+    return t if type(t) is QTensor else (t,) if t is not None else ()
 
 
 _I8, _F32 = torch.int8, torch.float32
@@ -477,7 +479,7 @@ def jf_linear_fwd_epilogue(X: QTensor, W: QTensor, Y: Optional[QTensor] = None, 
     _run("jf_linear_fwd_epilogue", lib.jf_linear_fwd_epilogue,
          (cx, cw, _f32_vector(bias, cols, "bias"), _activation(act), Rq, R, _NO_Q if Y is None else _operand(Y, "Y", _Q),
           _matrix(y, rows, cols, "y"), _NO_Q if P is None else _operand(P, "P", _Q)),
-         (X, W, Y, y, bias, residual, P), stream)
+         _device("jf_linear_fwd_epilogue", *X, *W, y, bias, *_parts(Y), *_parts(P), *_parts(residual)), stream)
 
 
 def jf_linear_dgrad_epilogue(dY: QTensor, W: QTensor, dX: Optional[QTensor] = None, dx: Optional[torch.Tensor] = None,
@@ -491,14 +493,14 @@ def jf_linear_dgrad_epilogue(dY: QTensor, W: QTensor, dX: Optional[QTensor] = No
     _run("jf_linear_dgrad_epilogue", lib.jf_linear_dgrad_epilogue,
          (cy, cw, _NO_CQ if pre is None else _operand(pre, "pre"), _activation(act), Rq, R,
           _NO_Q if dX is None else _operand(dX, "dX", _Q), _matrix(dx, rows, cols, "dx")),
-         (dY, W, dX, dx, pre, residual), stream)
+         _device("jf_linear_dgrad_epilogue", *dY, *W, dx, *_parts(dX), *_parts(pre), *_parts(residual)), stream)
 
 
 def jf_bias_grad(dY: QTensor, db: torch.Tensor, stream=None) -> None:
     """db (float32 [cols]) = the column sums of dY."""
     lib = load_library()
     cy = _operand(dY, "dY")
-    _run("jf_bias_grad", lib.jf_bias_grad, (cy, _f32_vector(db, cy.cols, "db")), (dY, db), stream)
+    _run("jf_bias_grad", lib.jf_bias_grad, (cy, _f32_vector(db, cy.cols, "db")), _device("jf_bias_grad", *dY, db), stream)
 
 
 def jf_rope_table(inv_freq, cos: torch.Tensor, sin: torch.Tensor, magnitude: float = 1.0, stream=None) -> None:
@@ -509,8 +511,8 @@ def jf_rope_table(inv_freq, cos: torch.Tensor, sin: torch.Tensor, magnitude: flo
         if t.dtype != torch.float32 or t.dim() != 2 or t.shape[1] != half or t.shape != cos.shape:
             raise ValueError(f"{what} must be float32 of shape (length, {half})")
     freq = (ctypes.c_double * max(half, 1))(*[float(f) for f in inv_freq])
-    _run("jf_rope_table", lib.jf_rope_table, (freq, half, float(magnitude), cos.shape[0], _ptr(cos), _ptr(sin)), (cos, sin),
-         stream)
+    _run("jf_rope_table", lib.jf_rope_table, (freq, half, float(magnitude), cos.shape[0], _ptr(cos), _ptr(sin)),
+         _device("jf_rope_table", cos, sin), stream)
 
 
 class QKVRope(NamedTuple):
@@ -586,7 +588,7 @@ def jf_qkv_rope_fwd(qkv: QTensor, a: QKVRope, q: Optional[torch.Tensor], k: Opti
     _run("jf_qkv_rope_fwd", lib.jf_qkv_rope_fwd,
          (_operand(qkv, "qkv"), _rope(a), _heads(q, a, a.q_heads, heads_first, dtype, "q"),
           _heads(k, a, a.kv_heads, heads_first, dtype, "k"), _heads(v, a, a.kv_heads, heads_first, dtype, "v"), _DTYPES[dtype]),
-         (qkv, q, k, v, a.cos, a.sin, a.positions, a.gamma_q, a.gamma_k), stream)
+         _device("jf_qkv_rope_fwd", *qkv, q, k, v, a.cos, a.sin, a.positions, a.gamma_q, a.gamma_k), stream)
 
 
 def jf_qkv_rope_bwd_workspace_bytes(rows: int, a: QKVRope) -> int:
@@ -597,15 +599,19 @@ def jf_qkv_rope_bwd(qkv: QTensor, a: QKVRope, dq, dk, dv, dqkv: QTensor, dgamma_
                     dgamma_k: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                     heads_first: bool = False, stream=None) -> None:
     """The gradient of jf_qkv_rope_fwd: dq, dk, dv to INT8 dqkv and the norm weights' gradients."""
-    lib = load_library()
+    _qkv_rope_bwd(load_library(), _rope(a), qkv, a, dq, dk, dv, dqkv, dgamma_q, dgamma_k, workspace, heads_first, stream)
+
+
+def _qkv_rope_bwd(lib, rope: _Rope, qkv, a, dq, dk, dv, dqkv, dgamma_q, dgamma_k, workspace, heads_first, stream) -> None:
     dtype = _qkv_dtype(dq, dk, dv)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _run("jf_qkv_rope_bwd", lib.jf_qkv_rope_bwd,
-         (_operand(qkv, "qkv"), _rope(a), _heads(dq, a, a.q_heads, heads_first, dtype, "dq"),
+         (_operand(qkv, "qkv"), rope, _heads(dq, a, a.q_heads, heads_first, dtype, "dq"),
           _heads(dk, a, a.kv_heads, heads_first, dtype, "dk"), _heads(dv, a, a.kv_heads, heads_first, dtype, "dv"), _DTYPES[dtype],
           _operand(dqkv, "dqkv", _Q), _f32_vector(dgamma_q, a.head_dim, "dgamma_q"),
           _f32_vector(dgamma_k, a.head_dim, "dgamma_k"), None if workspace is None else _ptr(workspace), nbytes),
-         (qkv, dq, dk, dv, dqkv, dgamma_q, dgamma_k, workspace, a.cos, a.sin, a.positions, a.gamma_q, a.gamma_k), stream)
+         _device("jf_qkv_rope_bwd", *qkv, dq, dk, dv, *dqkv, dgamma_q, dgamma_k, workspace, a.cos, a.sin, a.positions, a.gamma_q,
+                 a.gamma_k), stream)
 
 
 def jf_selftest_wait_timeout(limit_ns: int, stream=None) -> None:
@@ -801,12 +807,12 @@ def qkv_rope_bwd(qkv: QTensor, a: QKVRope, dq: torch.Tensor, dk: torch.Tensor, d
                  stream=None):
     """(dqkv, dgamma_q, dgamma_k) of qkv_rope: an INT8 gradient for the projection's backward, and the norm
     weights' gradients (None where there is no norm). The workspace is allocated here, per call."""
-    dev = qkv.q.device
+    lib, rope, dev = load_library(), _rope(a), qkv.q.device
     dqkv = empty_qtensor(qkv.rows, qkv.cols, dev)
     dgq = torch.empty(a.head_dim, dtype=torch.float32, device=dev) if a.gamma_q is not None else None
     dgk = torch.empty(a.head_dim, dtype=torch.float32, device=dev) if a.gamma_k is not None else None
     ws = None
     if dgq is not None or dgk is not None:
-        ws = torch.empty(max(jf_qkv_rope_bwd_workspace_bytes(qkv.rows, a), 0), dtype=torch.uint8, device=dev)
-    jf_qkv_rope_bwd(qkv, a, dq, dk, dv, dqkv, dgq, dgk, ws, heads_first, stream)
+        ws = torch.empty(max(lib.jf_qkv_rope_bwd_workspace_bytes(qkv.rows, rope), 0), dtype=torch.uint8, device=dev)
+    _qkv_rope_bwd(lib, rope, qkv, a, dq, dk, dv, dqkv, dgq, dgk, ws, heads_first, stream)
     return dqkv, dgq, dgk
