@@ -267,7 +267,9 @@ typedef struct {
 /*
  * Linear forward with bias, activation and residual in its epilogue:
  *   P = X W^T + bias,  Z = act(P) + R        (X [M, K], W [N, K], Z [M, N])
- * in fp32 from jf_linear_fwd's accumulators; nothing but the outputs reaches memory.
+ * in fp32 from jf_linear_fwd's products; nothing but the outputs reaches memory. Where M x N fills few SMs the
+ * fp32 sum over K is taken in up to 8 parts that are added in a fixed order (jf_linear_fwd adds in one run, so
+ * the two may differ in the last bits); the same call gives the same bits every time.
  *   bias  device fp32 [N], 16-byte aligned, or NULL
  *   Rq/R  the residual: an INT8 tensor (Rq.q) or a dense matrix (R.p), at most one of them (JF_ERR_ARG)
  *   Y     optional output: requant(Z) per 32x32 block (Y.q = NULL to skip it)

@@ -610,6 +610,7 @@ int epilogue_call(int mode, const jf_cqtensor& A, const jf_cqtensor& B, const fl
   g.y_ld = y.ld;
   g.bias = bias;
   g.act = int(act);
+  g.split_ok = true;
   if (want_saved) {
     g.act_q = saved.q;
     g.act_s = saved.s;

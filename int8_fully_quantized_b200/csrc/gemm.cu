@@ -52,6 +52,7 @@
 // Every mbarrier wait is bounded (ptx.cuh). On a timeout the warp that saw it sets the CTA's abort
 // flag; every other wait then gives up too and the roles end; in-flight copies and MMAs are drained
 // (bounded) before TMEM is freed.
+#include <cooperative_groups.h>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -66,6 +67,8 @@
 #include "quant.cuh"
 
 namespace jf {
+
+namespace cg = cooperative_groups;
 
 constexpr int BM = 128;             // tile rows = MMA M = TMEM lanes
 constexpr int BN = 128;             // tile cols = MMA N = TMEM columns of one accumulator
@@ -116,6 +119,7 @@ struct __align__(64) GemmParams {
   int rows, cols, kblocks;
   int tiles_m, tiles_n;
   int n_fast;   // tile order: 0 = row tiles vary fastest, 1 = column tiles vary fastest
+  int share;    // split contraction: pipeline stages of each CTA of a cluster
   EpilogueParams ep;
 };
 
@@ -128,12 +132,13 @@ struct __align__(64) GemmParams {
 struct TileWalk {
   int a, b, da, db, na;   // tile t = b na + a, a varying fastest
   bool n_fast;
-  __device__ __forceinline__ explicit TileWalk(const GemmParams& p)
+  // From tile `first` in steps of `step`.
+  __device__ __forceinline__ TileWalk(const GemmParams& p, int first, int step)
       : na(p.n_fast ? p.tiles_n : p.tiles_m), n_fast(p.n_fast != 0) {
-    a = int(blockIdx.x) % na;
-    b = int(blockIdx.x) / na;
-    da = int(gridDim.x) % na;
-    db = int(gridDim.x) / na;
+    a = first % na;
+    b = first / na;
+    da = step % na;
+    db = step / na;
   }
   __device__ __forceinline__ void next() {
     a += da;
@@ -197,7 +202,11 @@ __device__ __forceinline__ float scale_window(const float* __restrict__ base, in
   return (blk < nblk && kb < kblocks) ? __ldg(base + blk * s_blk + int64_t(kb) * s_k) : 0.0f;
 }
 
-template <bool A_MN, bool B_MN, int EPI, int NOUT>
+// SPLIT: a cluster of CTAs takes one tile, each a part of its contraction (p.share pipeline stages, in rank
+// order; a part may be empty). The sum warps write each 32 x 32 part into the shared memory of the CTA that
+// owns its block (distributed shared memory: written, not read, as nobody waits for a write; reading the parts
+// from there instead took 6 us more), and the owners' output warps add the parts in rank order.
+template <bool A_MN, bool B_MN, int EPI, int NOUT, bool SPLIT>
 __global__ void __launch_bounds__(Roles<NOUT>::kThreads, 1) gemm_i8_kernel(const __grid_constant__ GemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -244,15 +253,21 @@ __global__ void __launch_bounds__(Roles<NOUT>::kThreads, 1) gemm_i8_kernel(const
   }
   for (int i = threadIdx.x; i < BM * KB / 4; i += Roles<NOUT>::kThreads) reinterpret_cast<uint32_t*>(smem + SMEM_BIAS)[i] = 0x80808080u;
   fence_proxy_async_smem();   // the bias operand is read by the tensor core
+  const cg::cluster_group cluster = cg::this_cluster();
   tc_fence_before();
-  __syncthreads();
+  if constexpr (SPLIT) cluster.sync();   // every CTA has started: its shared memory may be written
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
-  const int kblocks = p.kblocks;
+  // this CTA's part of the contraction: blocks kb0 .. kb0 + kblocks - 1
+  const int rank = SPLIT ? int(cluster.block_rank()) : 0, parts = SPLIT ? int(cluster.num_blocks()) : 1;
+  const int kb0 = SPLIT ? rank * p.share * KBS : 0;
+  const int kblocks = SPLIT ? max(0, min(p.share * KBS, p.kblocks - kb0)) : p.kblocks;
   const int num_kstages = (kblocks + KBS - 1) / KBS;
   const int num_tiles = p.tiles_m * p.tiles_n;
-  const int my_tiles = blockIdx.x < num_tiles ? (num_tiles - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+  const int first_tile = int(blockIdx.x) / parts, tile_step = int(gridDim.x) / parts;
+  const int my_tiles = SPLIT ? 1 : first_tile < num_tiles ? (num_tiles - 1 - first_tile) / tile_step + 1 : 0;
   const int total_stages = my_tiles * num_kstages;   // this CTA's stages, in order
 
   if (warp < FIRST_SUM_WARP) {
@@ -261,7 +276,7 @@ __global__ void __launch_bounds__(Roles<NOUT>::kThreads, 1) gemm_i8_kernel(const
       // ------------------------------------------------------------------ producer warp
       if (lane == 0) {
         uint32_t pending = 0, pend_ph = 0;  // slots armed, and the parity armed
-        TileWalk at(p);
+        TileWalk at(p, first_tile, tile_step);
         int ks = 0, st = 0;
         uint32_t ph = 0;
         for (int g = 0; g < total_stages; ++g) {
@@ -272,7 +287,7 @@ __global__ void __launch_bounds__(Roles<NOUT>::kThreads, 1) gemm_i8_kernel(const
           mbar_arrive_expect_tx(&full[st], A_STAGE + B_STAGE);
           pending |= 1u << st;
           pend_ph = (pend_ph & ~(1u << st)) | (ph << st);
-          const int k0 = ks * KBS * KB;
+          const int k0 = (kb0 + ks * KBS) * KB;
           if (!A_MN) tma_load_2d(sA + st * A_STAGE, &p.tma_a, &full[st], k0, row0);
           else tma_load_2d(sA + st * A_STAGE, &p.tma_a, &full[st], row0, k0);
           if (!B_MN) tma_load_2d(sB + st * B_STAGE, &p.tma_b, &full[st], k0, col0);
@@ -353,12 +368,13 @@ __global__ void __launch_bounds__(Roles<NOUT>::kThreads, 1) gemm_i8_kernel(const
     float sa_n, sb0_n, sb1_n;
     auto load_scales = [&](const TileWalk& at, int w0, bool valid) {
       const int rbk = at.row() * (BM / 32) + sub, cbk = at.col() * (BN / 32) + cb0;
-      sa_n = scale_window(p.a_s, p.a_s_blk, p.a_s_k, rbk, valid ? nrb : 0, w0, kblocks, lane);
-      sb0_n = scale_window(p.b_s, p.b_s_blk, p.b_s_k, cbk, valid ? ncb : 0, w0, kblocks, lane);
-      sb1_n = scale_window(p.b_s, p.b_s_blk, p.b_s_k, cbk + 1, valid ? ncb : 0, w0, kblocks, lane);
+      sa_n = scale_window(p.a_s, p.a_s_blk, p.a_s_k, rbk, valid ? nrb : 0, kb0 + w0, kb0 + kblocks, lane);
+      sb0_n = scale_window(p.b_s, p.b_s_blk, p.b_s_k, cbk, valid ? ncb : 0, kb0 + w0, kb0 + kblocks, lane);
+      sb1_n = scale_window(p.b_s, p.b_s_blk, p.b_s_k, cbk + 1, valid ? ncb : 0, kb0 + w0, kb0 + kblocks, lane);
     };
-    TileWalk at(p);                       // the tile of the scales loaded last
+    TileWalk at(p, first_tile, tile_step);                       // the tile of the scales loaded last
     load_scales(at, 0, my_tiles > 0);
+    const int row_blk0 = at.row() * (BM / 32), col_blk0 = at.col() * (BN / 32);   // the first tile's blocks
     int gi = 0;                           // groups consumed so far
     bool alive = true;
     for (int tile = 0; tile < my_tiles; ++tile) {
@@ -407,6 +423,16 @@ __global__ void __launch_bounds__(Roles<NOUT>::kThreads, 1) gemm_i8_kernel(const
         }
       }
       if (!alive) break;
+      if constexpr (SPLIT) {
+        // the parts of the valid blocks to the CTAs that add them: block b to rank b % parts
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int b = 2 * w + h, owner = b & (parts - 1);
+          if (row_blk0 + sub < nrb && col_blk0 + cb0 + h < ncb)
+            block_to_smem(acc[h], cluster.map_shared_rank(smem + SMEM_OUT + (b - owner + rank) * 4096, owner), lane);
+        }
+        break;
+      }
       // the finished blocks to the output warps, and on to the next tile
       const bool room = mbar_wait_often(&oempty[w], (uint32_t(tile) & 1u) ^ 1u, abort_flag, p.status);
       if (!__all_sync(0xffffffffu, room)) break;
@@ -420,9 +446,9 @@ __global__ void __launch_bounds__(Roles<NOUT>::kThreads, 1) gemm_i8_kernel(const
     if constexpr (Roles<NOUT>::kOut > Roles<NOUT>::kLaunch) setmaxnreg_inc<Roles<NOUT>::kOut>();
     else setmaxnreg_dec<Roles<NOUT>::kOut>();
     const int nrb = p.rows >> 5, ncb = p.cols >> 5;
-    TileWalk at(p);
+    TileWalk at(p, first_tile, tile_step);
     bool alive = true;
-    for (int tile = 0; alive && tile < my_tiles; ++tile, at.next()) {
+    for (int tile = 0; !SPLIT && alive && tile < my_tiles; ++tile, at.next()) {
       for (int w = warp - FIRST_OUT_WARP; w < NUM_SUM_WARPS; w += NOUT) {
         const bool good = mbar_wait_often(&ofull[w], uint32_t(tile) & 1u, abort_flag, p.status);
         alive = __all_sync(0xffffffffu, good);
@@ -441,6 +467,27 @@ __global__ void __launch_bounds__(Roles<NOUT>::kThreads, 1) gemm_i8_kernel(const
         if (lane == 0) mbar_arrive(&oempty[w]);
       }
     }
+    if constexpr (SPLIT) {
+      cluster.sync();                     // every part is where it is added
+      const bool whole = *abort_flag == 0u;
+      for (int b = rank + parts * (warp - FIRST_OUT_WARP); whole && b < 16; b += parts * NOUT) {
+        const int w = b >> 1, rbk = at.row() * (BM / 32) + (w & 3), cbk = at.col() * (BN / 32) + (w >> 2) * 2 + (b & 1);
+        if (rbk >= nrb || cbk >= ncb) continue;
+        uint8_t* blk = smem + SMEM_OUT + (b - rank) * 4096;   // the parts in rank order
+        float v[32], part[32];
+        block_from_smem(v, blk, lane);
+        for (int r = 1; r < parts; ++r) {
+          block_from_smem(part, blk + r * 4096, lane);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) add_x2(v[i], v[i + 1], part[i], part[i + 1], v[i], v[i + 1]);
+        }
+        __syncwarp();                     // the block's memory is the warp's staging area from here on
+        block_epilogue<EPI>(p.ep, v, rbk, cbk, ncb, blk, lane);
+      }
+    }
+  }
+  if constexpr (SPLIT) {
+    if (warp < FIRST_OUT_WARP) cluster.sync();
   }
 
   tc_fence_before();
@@ -624,10 +671,10 @@ static bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool A_MN, bool B_MN, int EPI, int NOUT>
-static cudaError_t run(const GemmParams& prm, int grid, cudaStream_t st) {
+template <bool A_MN, bool B_MN, int EPI, int NOUT, bool SPLIT>
+static cudaError_t run(const GemmParams& prm, int grid, int parts, cudaStream_t st) {
   static unsigned long long attr_set = 0;  // one bit per device ordinal
-  auto kern = gemm_i8_kernel<A_MN, B_MN, EPI, NOUT>;
+  auto kern = gemm_i8_kernel<A_MN, B_MN, EPI, NOUT, SPLIT>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -636,6 +683,20 @@ static cudaError_t run(const GemmParams& prm, int grid, cudaStream_t st) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
     attr_set |= bit;
+  }
+  if constexpr (SPLIT) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid * parts), 1, 1);
+    cfg.blockDim = dim3(Roles<NOUT>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(parts);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, prm);
   }
   kern<<<grid, Roles<NOUT>::kThreads, SMEM_BYTES, st>>>(prm);
   return cudaGetLastError();
@@ -702,11 +763,27 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t st) {
   // warps down (8192 x 16384 x 4096 1792 us against 1727).
   const bool long_epilogue = g.pre_q != nullptr || g.act == kActGelu || (g.mode == kDgrad && g.act != kActNone);
   const bool out8 = long_epilogue && kbn <= 64;
-  if (g.mode == kFwd)
-    return out8 ? run<false, false, kEpiForward, 8>(prm, grid, st) : run<false, false, kEpiForward, 4>(prm, grid, st);
-  if (g.mode == kDgrad)
-    return out8 ? run<false, true, kEpiGrad, 8>(prm, grid, st) : run<false, true, kEpiGrad, 4>(prm, grid, st);
-  return run<true, true, kEpiPlain, 4>(prm, grid, st);
+  // Few tiles leave SMs idle: the contraction is then split over clusters of 2, 4 or 8 CTAs, each with at least
+  // one pipeline stage (two in clusters of 8, where one costs 1 us more than clusters of 4), as long as all
+  // clusters run at once: a GPC's last SMs do not make up a whole cluster (of 148 SMs, 33 clusters of 4 and 15
+  // of 8 are resident), which the 5 clusters to spare allow for. Undivided and split, us (bias, SiLU, bf16):
+  // 32 x 4096 x 4096 45 and 21, 32 x 16384 x 4096 135 and 45, 352 x 1056 x 544 20.5 and 16.4, 256^3 17.2 and
+  // 15.5, 1024 x 4096 x 1024 45 and 31. The sum's order, and with it the last bits, differ from the undivided
+  // sum's, so only the calls that were born with it take it (split_ok).
+  const int stages = int((kbn + KBS - 1) / KBS);
+  int parts = 1;
+  for (int c = 2; g.split_ok && c <= 8; c *= 2)
+    if ((tiles + 5) * c <= sm_count && stages >= (c < 8 ? c : 2 * c)) parts = c;
+  prm.share = (stages + parts - 1) / parts;
+  if (g.mode == kFwd) {
+    if (parts > 1) return run<false, false, kEpiForward, 4, true>(prm, tiles, parts, st);
+    return out8 ? run<false, false, kEpiForward, 8, false>(prm, grid, 1, st) : run<false, false, kEpiForward, 4, false>(prm, grid, 1, st);
+  }
+  if (g.mode == kDgrad) {
+    if (parts > 1) return run<false, true, kEpiGrad, 4, true>(prm, tiles, parts, st);
+    return out8 ? run<false, true, kEpiGrad, 8, false>(prm, grid, 1, st) : run<false, true, kEpiGrad, 4, false>(prm, grid, 1, st);
+  }
+  return run<true, true, kEpiPlain, 4, false>(prm, grid, 1, st);
 }
 
 cudaError_t launch_gemm_s32(const int8_t* a, const int8_t* b, int32_t* c, int64_t M, int64_t N, int64_t K,

@@ -124,6 +124,7 @@ struct GemmArgs {
   const float* act_s;
   int8_t* pre_q;              // forward: the re-quantized pre-activation
   float* pre_s;
+  bool split_ok;              // few tiles may split a long contraction (another order of the fp32 sum)
   const void* res;            // residual: dense of DenseType res_type, or kResI8 codes with scales res_s
   const float* res_s;
   int res_type;

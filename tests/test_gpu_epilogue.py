@@ -98,6 +98,49 @@ def test_input_gradient(M, K, N, act, res):
     check_status()
 
 
+# few output tiles and a long contraction, which clusters of CTAs share: 8 parts; 8 of which two are empty; 8 with a
+# last one of a single block; 4 of which one is empty; 4; 2 of one stage each
+@pytest.mark.parametrize("M,N,K", [(32, 64, 4096), (160, 352, 2080), (32, 32, 3616), (352, 544, 1056), (128, 4096, 544), (1024, 1024, 256)])
+def test_shared_contraction(M, N, K):
+    """Forward and input gradient as above, the same bits at every call, on two streams at once and replayed."""
+    g = _gen(M + N + K)
+    X, W, dY, WT = _qt(g, M, K), _qt(g, N, K, 0.05), _qt(g, M, K, 1e-2), _qt(g, K, N, 0.05)
+    P = _qt(g, M, N, 1.5)
+    bias = torch.randn(N, generator=g, device="cuda")
+    r = torch.randn(M, N, generator=g, device="cuda")
+    xv, wv, dv, tv = B.value(*X), B.value(*W), B.value(*dY), B.value(*WT)
+    p = xv @ wv.t() + bias.double()
+    z = B.act(p, "gelu") + r.double()
+    tol = 1.13 * GEMM_RTOL * (xv.abs() @ wv.abs().t()) + 2.0 ** -18 * (p.abs() + z.abs() + r.double().abs())
+    y = jf.linear_fwd_epilogue(X, W, bias, "gelu", r, out_dtype=torch.float32)
+    _close(y, z, tol, "dense")
+    Y, pre = jf.linear_fwd_epilogue(X, W, bias, "gelu", r, want_pre=True)
+    q, s = B.quantize(y)
+    assert torch.equal(q, Y.q) and torch.equal(s, Y.s)
+    _codes_close(pre, p, "P")
+    d = jf.linear_dgrad_epilogue(dY, WT, P, "gelu", r, out_dtype=torch.float32)
+    dz = (dv @ tv) * B.act_grad(B.value(*P), "gelu") + r.double()
+    _close(d, dz, 1.13 * GEMM_RTOL * (dv.abs() @ tv.abs()) + 2.0 ** -18 * ((dv @ tv).abs() + dz.abs() + r.double().abs()), "input gradient")
+    side = [torch.cuda.Stream() for _ in range(2)]
+    ys = [torch.empty_like(y) for _ in range(8)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(ys):
+        if i % 2:
+            jf.jf_linear_dgrad_epilogue(dY, WT, dx=o, pre=P, act="gelu", residual=r, stream=side[i // 2 % 2])
+        else:
+            jf.jf_linear_fwd_epilogue(X, W, y=o, bias=bias, act="gelu", residual=r, stream=side[i // 2 % 2])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, d if i % 2 else y) for i, o in enumerate(ys))
+    out, graph = torch.empty_like(y), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        jf.jf_linear_fwd_epilogue(X, W, y=out, bias=bias, act="gelu", residual=r)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, y)
+    check_status()
+
+
 @pytest.mark.parametrize("act", B.ACTS)
 def test_activation_gradient_against_differences(act):
     """dY = I in 32 x 32 blocks through W = I: Z = act'(P) itself, against central differences of the
