@@ -170,6 +170,10 @@ def empty_qtensor(rows: int, cols: int, device="cuda") -> QTensor:
                    torch.empty((rows // 32, cols // 32), dtype=torch.float32, device=device))
 
 
+def _empty_like(t: QTensor, rows: int, cols: int) -> QTensor:
+    return QTensor(t.q.new_empty((rows, cols)), t.s.new_empty((rows // 32, cols // 32)))
+
+
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     if t is None:
         return None
@@ -725,10 +729,10 @@ def linear_fwd_epilogue(X: QTensor, W: QTensor, bias: Optional[torch.Tensor] = N
     """act(X W^T + bias) + residual as INT8 blocks, or as a dense matrix of out_dtype; with ``want_pre`` also
     the re-quantized pre-activation X W^T + bias, for linear_dgrad_epilogue. The residual is a QTensor or a
     dense matrix of any supported dtype."""
-    dev = X.q.device
-    Y = empty_qtensor(X.rows, W.rows, dev) if out_dtype is None else None
-    y = torch.empty((X.rows, W.rows), dtype=out_dtype, device=dev) if out_dtype is not None else None
-    P = empty_qtensor(X.rows, W.rows, dev) if want_pre else None
+    rows, cols = X.rows, W.rows
+    Y = _empty_like(X, rows, cols) if out_dtype is None else None
+    y = X.q.new_empty((rows, cols), dtype=out_dtype) if out_dtype is not None else None
+    P = _empty_like(X, rows, cols) if want_pre else None
     jf_linear_fwd_epilogue(X, W, Y, y, bias, act, residual, P, stream)
     out = Y if y is None else y
     return (out, P) if want_pre else out
@@ -737,16 +741,16 @@ def linear_fwd_epilogue(X: QTensor, W: QTensor, bias: Optional[torch.Tensor] = N
 def linear_dgrad_epilogue(dY: QTensor, W: QTensor, pre: Optional[QTensor] = None, act: str = "none", residual=None,
                           out_dtype: Optional[torch.dtype] = None, stream=None):
     """(dY W) * act'(pre) + residual as INT8 blocks, or as a dense matrix of out_dtype."""
-    dev = dY.q.device
-    dX = empty_qtensor(dY.rows, W.cols, dev) if out_dtype is None else None
-    dx = torch.empty((dY.rows, W.cols), dtype=out_dtype, device=dev) if out_dtype is not None else None
+    rows, cols = dY.rows, W.cols
+    dX = _empty_like(dY, rows, cols) if out_dtype is None else None
+    dx = dY.q.new_empty((rows, cols), dtype=out_dtype) if out_dtype is not None else None
     jf_linear_dgrad_epilogue(dY, W, dX, dx, pre, act, residual, stream)
     return dX if dx is None else dx
 
 
 def bias_grad(dY: QTensor, stream=None) -> torch.Tensor:
     """The bias gradient (float32 [cols]): the column sums of the INT8 gradient dY."""
-    db = torch.empty(dY.cols, dtype=torch.float32, device=dY.q.device)
+    db = dY.s.new_empty(dY.cols)
     jf_bias_grad(dY, db, stream)
     return db
 
@@ -797,8 +801,8 @@ def qkv_rope(qkv: QTensor, a: QKVRope, dtype: torch.dtype = torch.bfloat16, head
     """(q, k, v) for attention from the INT8 output of the QKV projection, [batch, seq, heads, head_dim] (with
     heads_first [batch, heads, seq, head_dim]): queries and keys normed per head (where ``a`` has weights) and
     rotated, values dequantized."""
-    out = [torch.empty((a.batch, n, a.seq, a.head_dim) if heads_first else (a.batch, a.seq, n, a.head_dim), dtype=dtype,
-                       device=qkv.q.device) for n in (a.q_heads, a.kv_heads, a.kv_heads)]
+    out = [qkv.q.new_empty((a.batch, n, a.seq, a.head_dim) if heads_first else (a.batch, a.seq, n, a.head_dim), dtype=dtype)
+           for n in (a.q_heads, a.kv_heads, a.kv_heads)]
     jf_qkv_rope_fwd(qkv, a, *out, heads_first, stream)
     return tuple(out)
 
@@ -807,12 +811,12 @@ def qkv_rope_bwd(qkv: QTensor, a: QKVRope, dq: torch.Tensor, dk: torch.Tensor, d
                  stream=None):
     """(dqkv, dgamma_q, dgamma_k) of qkv_rope: an INT8 gradient for the projection's backward, and the norm
     weights' gradients (None where there is no norm). The workspace is allocated here, per call."""
-    lib, rope, dev = load_library(), _rope(a), qkv.q.device
-    dqkv = empty_qtensor(qkv.rows, qkv.cols, dev)
-    dgq = torch.empty(a.head_dim, dtype=torch.float32, device=dev) if a.gamma_q is not None else None
-    dgk = torch.empty(a.head_dim, dtype=torch.float32, device=dev) if a.gamma_k is not None else None
+    lib, rope = load_library(), _rope(a)
+    dqkv = _empty_like(qkv, qkv.rows, qkv.cols)
+    dgq = qkv.s.new_empty(a.head_dim) if a.gamma_q is not None else None
+    dgk = qkv.s.new_empty(a.head_dim) if a.gamma_k is not None else None
     ws = None
     if dgq is not None or dgk is not None:
-        ws = torch.empty(max(lib.jf_qkv_rope_bwd_workspace_bytes(qkv.rows, rope), 0), dtype=torch.uint8, device=dev)
+        ws = qkv.q.new_empty(max(lib.jf_qkv_rope_bwd_workspace_bytes(qkv.rows, rope), 0), dtype=torch.uint8)
     _qkv_rope_bwd(lib, rope, qkv, a, dq, dk, dv, dqkv, dgq, dgk, ws, heads_first, stream)
     return dqkv, dgq, dgk
