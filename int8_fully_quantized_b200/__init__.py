@@ -12,6 +12,7 @@ A quantized tensor is a pair ``QTensor(q, s)``: ``q`` int8 [rows, cols] codes an
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import math
@@ -168,6 +169,18 @@ class QTensor(NamedTuple):
 def empty_qtensor(rows: int, cols: int, device="cuda") -> QTensor:
     return QTensor(torch.empty((rows, cols), dtype=torch.int8, device=device),
                    torch.empty((rows // 32, cols // 32), dtype=torch.float32, device=device))
+
+
+def _on(stream, device: torch.device):
+    """The context of a stream in which a helper allocates: memory the caching allocator hands out belongs to one
+    stream, and what the call frees again (a workspace) may still be in use there."""
+    if not _has_cuda():
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device)
+    elif device.type == "cuda" and device.index is not None and stream.device_index != device.index:
+        raise ValueError(f"a stream of cuda:{stream.device_index} for tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _empty_like(t: QTensor, rows: int, cols: int) -> QTensor:
@@ -729,11 +742,14 @@ def linear_fwd_epilogue(X: QTensor, W: QTensor, bias: Optional[torch.Tensor] = N
     """act(X W^T + bias) + residual as INT8 blocks, or as a dense matrix of out_dtype; with ``want_pre`` also
     the re-quantized pre-activation X W^T + bias, for linear_dgrad_epilogue. The residual is a QTensor or a
     dense matrix of any supported dtype."""
+    if stream is not None:
+        with _on(stream, X.q.device):
+            return linear_fwd_epilogue(X, W, bias, act, residual, want_pre, out_dtype)
     rows, cols = X.rows, W.rows
     Y = _empty_like(X, rows, cols) if out_dtype is None else None
     y = X.q.new_empty((rows, cols), dtype=out_dtype) if out_dtype is not None else None
     P = _empty_like(X, rows, cols) if want_pre else None
-    jf_linear_fwd_epilogue(X, W, Y, y, bias, act, residual, P, stream)
+    jf_linear_fwd_epilogue(X, W, Y, y, bias, act, residual, P)
     out = Y if y is None else y
     return (out, P) if want_pre else out
 
@@ -741,17 +757,23 @@ def linear_fwd_epilogue(X: QTensor, W: QTensor, bias: Optional[torch.Tensor] = N
 def linear_dgrad_epilogue(dY: QTensor, W: QTensor, pre: Optional[QTensor] = None, act: str = "none", residual=None,
                           out_dtype: Optional[torch.dtype] = None, stream=None):
     """(dY W) * act'(pre) + residual as INT8 blocks, or as a dense matrix of out_dtype."""
+    if stream is not None:
+        with _on(stream, dY.q.device):
+            return linear_dgrad_epilogue(dY, W, pre, act, residual, out_dtype)
     rows, cols = dY.rows, W.cols
     dX = _empty_like(dY, rows, cols) if out_dtype is None else None
     dx = dY.q.new_empty((rows, cols), dtype=out_dtype) if out_dtype is not None else None
-    jf_linear_dgrad_epilogue(dY, W, dX, dx, pre, act, residual, stream)
+    jf_linear_dgrad_epilogue(dY, W, dX, dx, pre, act, residual)
     return dX if dx is None else dx
 
 
 def bias_grad(dY: QTensor, stream=None) -> torch.Tensor:
     """The bias gradient (float32 [cols]): the column sums of the INT8 gradient dY."""
+    if stream is not None:
+        with _on(stream, dY.q.device):
+            return bias_grad(dY)
     db = dY.s.new_empty(dY.cols)
-    jf_bias_grad(dY, db, stream)
+    jf_bias_grad(dY, db)
     return db
 
 
@@ -791,9 +813,12 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none",
 
 def rope_table(length: int, inv_freq, magnitude: float = 1.0, device="cuda", stream=None):
     """(cos, sin): the float32 tables [length, len(inv_freq)] of a program's rotary positions, kept for all calls."""
+    if stream is not None:
+        with _on(stream, torch.device(device)):
+            return rope_table(length, inv_freq, magnitude, device)
     cos = torch.empty((length, len(inv_freq)), dtype=torch.float32, device=device)
     sin = torch.empty_like(cos)
-    jf_rope_table(inv_freq, cos, sin, magnitude, stream)
+    jf_rope_table(inv_freq, cos, sin, magnitude)
     return cos, sin
 
 
@@ -801,9 +826,12 @@ def qkv_rope(qkv: QTensor, a: QKVRope, dtype: torch.dtype = torch.bfloat16, head
     """(q, k, v) for attention from the INT8 output of the QKV projection, [batch, seq, heads, head_dim] (with
     heads_first [batch, heads, seq, head_dim]): queries and keys normed per head (where ``a`` has weights) and
     rotated, values dequantized."""
+    if stream is not None:
+        with _on(stream, qkv.q.device):
+            return qkv_rope(qkv, a, dtype, heads_first)
     out = [qkv.q.new_empty((a.batch, n, a.seq, a.head_dim) if heads_first else (a.batch, a.seq, n, a.head_dim), dtype=dtype)
            for n in (a.q_heads, a.kv_heads, a.kv_heads)]
-    jf_qkv_rope_fwd(qkv, a, *out, heads_first, stream)
+    jf_qkv_rope_fwd(qkv, a, *out, heads_first)
     return tuple(out)
 
 
@@ -811,6 +839,9 @@ def qkv_rope_bwd(qkv: QTensor, a: QKVRope, dq: torch.Tensor, dk: torch.Tensor, d
                  stream=None):
     """(dqkv, dgamma_q, dgamma_k) of qkv_rope: an INT8 gradient for the projection's backward, and the norm
     weights' gradients (None where there is no norm). The workspace is allocated here, per call."""
+    if stream is not None:
+        with _on(stream, qkv.q.device):
+            return qkv_rope_bwd(qkv, a, dq, dk, dv, heads_first)
     lib, rope = load_library(), _rope(a)
     dqkv = _empty_like(qkv, qkv.rows, qkv.cols)
     dgq = qkv.s.new_empty(a.head_dim) if a.gamma_q is not None else None
@@ -818,5 +849,5 @@ def qkv_rope_bwd(qkv: QTensor, a: QKVRope, dq: torch.Tensor, dk: torch.Tensor, d
     ws = None
     if dgq is not None or dgk is not None:
         ws = qkv.q.new_empty(max(lib.jf_qkv_rope_bwd_workspace_bytes(qkv.rows, rope), 0), dtype=torch.uint8)
-    _qkv_rope_bwd(lib, rope, qkv, a, dq, dk, dv, dqkv, dgq, dgk, ws, heads_first, stream)
+    _qkv_rope_bwd(lib, rope, qkv, a, dq, dk, dv, dqkv, dgq, dgk, ws, heads_first, None)
     return dqkv, dgq, dgk

@@ -538,11 +538,14 @@ namespace {
 
 bool dtype_ok(jf_dtype dt) { return dt == JF_F32 || dt == JF_BF16 || dt == JF_F16; }
 
+// More elements than an address space has bytes: extents below it do not overflow.
+constexpr int64_t kMaxElements = int64_t(1) << 50;
+
 // A dense [rows, cols] operand of the epilogue calls, and the bytes from its first to its last element.
-int check_matrix(const void* p, jf_dtype dt, int64_t ld, int64_t cols) {
+int check_matrix(const void* p, jf_dtype dt, int64_t ld, int64_t rows, int64_t cols) {
   if (p == nullptr) return JF_OK;
   if (!dtype_ok(dt)) return JF_ERR_DTYPE;
-  if (ld < cols || ld >= (int64_t(1) << 40)) return JF_ERR_SHAPE;
+  if (ld < cols || ld >= kMaxElements || (rows > 1 && ld > kMaxElements / (rows - 1))) return JF_ERR_SHAPE;
   if (!aligned(p, 16) || (ld * elem_size(dt)) % 16 != 0) return JF_ERR_ALIGN;
   return JF_OK;
 }
@@ -565,8 +568,8 @@ int epilogue_call(int mode, const jf_cqtensor& A, const jf_cqtensor& B, const fl
     if ((st = check_cq(Rq)) != JF_OK) return st;
     if (Rq.rows != rows || Rq.cols != cols) return JF_ERR_SHAPE;
   }
-  if ((st = check_matrix(R.p, R.dt, R.ld, cols)) != JF_OK) return st;
-  if ((st = check_matrix(y.p, y.dt, y.ld, cols)) != JF_OK) return st;
+  if ((st = check_matrix(R.p, R.dt, R.ld, rows, cols)) != JF_OK) return st;
+  if ((st = check_matrix(y.p, y.dt, y.ld, rows, cols)) != JF_OK) return st;
   const jf_qtensor* const outs_q[2] = {&Y, &pre};
   for (const jf_qtensor* o : outs_q) {
     if (o->q == nullptr) continue;
@@ -655,7 +658,7 @@ int check_heads(const void* p, const int64_t (&stride)[3], const int64_t (&size)
   int64_t last = d - 1;
   for (int k = 0; k < 3; ++k) {
     if (size[k] == 1) continue;
-    if (stride[k] < 0 || stride[k] >= (int64_t(1) << 40)) return JF_ERR_SHAPE;
+    if (stride[k] < 0 || stride[k] > kMaxElements / (size[k] - 1)) return JF_ERR_SHAPE;
     if ((stride[k] * es) % 16 != 0) return JF_ERR_ALIGN;
     last += stride[k] * (size[k] - 1);
   }

@@ -113,9 +113,6 @@ __device__ __forceinline__ void mbar_wait_teardown(uint64_t* bar, uint32_t parit
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
-__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
 
 // Register split of a warp-specialized kernel (whole warpgroups; the sum over the CTA's threads must not
 // exceed what it was launched with).

@@ -157,6 +157,14 @@ def test_qkv_refusals(lib):
     assert _qkv(lib, rope(batch=0)) == 0
 
 
+def test_strides_past_any_address_space(lib):
+    """Strides whose products would overflow 64 bits are refused instead of wrapping into a small extent."""
+    assert _fwd(lib, y=mat(6, 1 << 58)) == SHAPE and _fwd(lib, R=mat(6, 1 << 58), y=NOM) == SHAPE
+    for bad in (dict(hs=1 << 58), dict(ss=1 << 58), dict(bs=1 << 58), dict(bs=1 << 62)):
+        assert _qkv(lib, rope(), q=heads(10, **bad)) == SHAPE, bad
+        assert _qkv_bwd(lib, rope(), v=heads(12, **bad) if "hs" not in bad else heads(12, ss=1 << 59)) == SHAPE, bad
+
+
 def test_rope_table_refusals(lib):
     f = (ctypes.c_double * 129)()
     assert lib.jf_rope_table(f, 0, 1.0, 4, at(1), at(2), None) == SHAPE

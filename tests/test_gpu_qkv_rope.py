@@ -310,3 +310,36 @@ def test_rope_table(length, half):
     ang = torch.arange(length, dtype=torch.float64)[:, None] * torch.tensor(f, dtype=torch.float64)
     for got, ref in ((cos, 1.25 * ang.cos()), (sin, 1.25 * ang.sin())):
         assert ((got.cpu().double() - ref).abs() <= 2.0 ** -24 * ref.abs() * 1.001 + 2.0 ** -35).all()
+
+
+def test_helpers_allocate_on_the_stream_they_run_on(monkeypatch):
+    """The workspace that qkv_rope_bwd frees on return must not go to the next allocation of another stream while
+    the kernels may still use it; the outputs of every helper equal those of the current stream."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    cos, sin = jf.rope_table(64, jf.rope_frequencies(64)[0])
+    gamma = torch.ones(64, device="cuda")
+    a = jf.QKVRope(2, 64, 4, 2, 64, cos, sin, gamma_q=gamma, gamma_k=gamma)
+    x = jf.quantize_block(torch.randn(128, 512, device="cuda", generator=g))
+    want = jf.qkv_rope(x, a)
+    want_b = jf.qkv_rope_bwd(x, a, *want)
+    side, seen, inner = torch.cuda.Stream(), [], jf._qkv_rope_bwd
+
+    def spy(*args):
+        seen.append((args[10].data_ptr(), args[10].numel(), torch.cuda.current_stream().cuda_stream))
+        return inner(*args)
+
+    monkeypatch.setattr(jf, "_qkv_rope_bwd", spy)
+    torch.cuda.synchronize()
+    for s in (side, side.cuda_stream):
+        q, k, v = jf.qkv_rope(x, a, stream=s)
+        dx, dgq, dgk = jf.qkv_rope_bwd(x, a, q, k, v, stream=s)
+        ptr, n, on = seen[-1]
+        later = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        assert on == side.cuda_stream and all(t.data_ptr() != ptr for t in later)
+        side.synchronize()
+        for got, ref in zip((q, k, v, dx.q, dx.s, dgq, dgk), (*want, *want_b[0], *want_b[1:])):
+            assert torch.equal(got, ref)
+    c2, s2 = jf.rope_table(64, jf.rope_frequencies(64)[0], stream=side)
+    side.synchronize()
+    assert torch.equal(c2, cos) and torch.equal(s2, sin)
+    check_status()
