@@ -3,14 +3,16 @@
 //   input gradient   Z = (dY W) * act'(P) + R                  with P the saved INT8 pre-activation
 // Z leaves re-quantized per 32x32 block or rounded once to a dense fp32 / bf16 / fp16 matrix.
 //
-// One warp holds two horizontally adjacent 32x32 blocks of the finished fp32 tile, lane = row, and takes
-// them one after the other through one copy of the code (a loop that is not unrolled: two copies pushed
-// registers of the GEMM's main loop into memory, 5-8% of the whole kernel). A lane's own 32 to 128 bytes
-// of a row are contiguous but the 32 lanes' rows are far apart: direct 16-byte accesses would touch 32
-// half-used sectors each. Every matrix access here goes through a 2 KB shared-memory staging area per
-// warp instead, as 32 rows of 32 or 64 bytes: two or four neighbouring lanes move a row's bytes. Row r
+// An output warp takes one finished 32x32 fp32 block at a time, lane = row. A lane's own 32 to 128 bytes of a
+// row are contiguous but the 32 lanes' rows are far apart: direct 16-byte accesses would touch 32 half-used
+// sectors each. Every matrix access here goes through the block's own shared memory (free once the block is in
+// registers) instead, as 32 rows of 32 or 64 bytes: two or four neighbouring lanes move a row's bytes. Row r
 // keeps its 16-byte chunk c at chunk position c ^ swizzle(r), so both sides of the transposition are
 // free of bank conflicts.
+//
+// What bounds it: the chain of one warp (shared memory -> absmax -> scale -> codes -> shared memory -> global
+// memory) beside two sum warps of the same sub-partition, ~1900 cycles a block, which the sum warps' ~460
+// cycles per contraction block cover from a contraction of 512 on (4096 x 256 x 4096 is bound by it: 41 us).
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -21,8 +23,6 @@
 #include "quant.cuh"
 
 namespace jf {
-
-constexpr int kStageBytes = 2048;   // staging of one epilogue warp: 32 rows x 64 bytes
 
 // Which epilogue a kernel carries: none of the extras (weight gradient), a forward, an input gradient.
 enum Epilogue { kEpiPlain = 0, kEpiForward = 1, kEpiGrad = 2 };
@@ -88,12 +88,15 @@ __device__ __forceinline__ void rows_load(const uint8_t* g, int64_t ld, uint32_t
 
 // Re-quantize one block (lane = row) and write its codes (q: its first code) and its scale.
 __device__ __forceinline__ void store_codes(const float (&v)[32], int8_t* q, int64_t ld, float* s, uint8_t* sm, int lane) {
-  float m = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));
-  const BlockQuant bq = block_quant(warp_max_nonneg(m));
+  const BlockQuant bq = block_quant_approx(warp_max_nonneg(absmax32(v)));
   uint32_t w[8];
-  quant_pack<32>(v, bq, w);
+  // halves: a test per 8 values or for all 32 at once is 1-2% slower for the whole kernel (4096 x 1024 x 4096, GELU)
+#pragma unroll
+  for (int k = 0; k < 32; k += 16) {
+    float far = bq.mode != 2 ? 1.0f : 0.0f;
+    codes_fast<16>(v + k, bq.inv, w + k / 4, far);
+    if (!(far < kFarLimit)) codes_exact<16>(v + k, bq.s, w + k / 4);
+  }
   if (lane == 0) *s = bq.s;
   rows_store<2>(reinterpret_cast<uint8_t*>(q), ld, w, sm, lane);
 }

@@ -757,12 +757,11 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t st) {
   prm.ep.y = static_cast<uint8_t*>(g.y);
   prm.ep.y_type = g.y_type;
   prm.ep.y_ld = g.y_ld * bytes(g.y_type);
-  // An epilogue with two re-quantizations, an activation gradient or the exact GELU takes 4 output warps about
-  // as long as 64 contraction blocks of main loop: below that 8 of them are faster (4096 x 1024 x 4096 with
-  // GELU and both outputs 103 us against 111, its input gradient 92 against 102), above they only slow the sum
-  // warps down (8192 x 16384 x 4096 1792 us against 1727).
-  const bool long_epilogue = g.pre_q != nullptr || g.act == kActGelu || (g.mode == kDgrad && g.act != kActNone);
-  const bool out8 = long_epilogue && kbn <= 64;
+  // The exact GELU (an erfc per element) takes 4 output warps longer than 64 contraction blocks take the sum warps:
+  // up to there 8 of them are faster (4096 x 1024 x 4096 119 us against 131, 4096 x 2048 x 4096 154 against 160),
+  // beyond they only slow the sum warps down. Every other epilogue keeps up with 4 (4096 x 1024 x 4096 with GELU
+  // and both outputs 92 us against 98).
+  const bool out8 = g.act == kActGelu && kbn <= 64;
   // Few tiles leave SMs idle: the contraction is then split over clusters of 2, 4 or 8 CTAs, each with at least
   // one pipeline stage (two in clusters of 8, where one costs 1 us more than clusters of 4), as long as all
   // clusters run at once: a GPC's last SMs do not make up a whole cluster (of 148 SMs, 33 clusters of 4 and 15
@@ -781,7 +780,7 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t st) {
   }
   if (g.mode == kDgrad) {
     if (parts > 1) return run<false, true, kEpiGrad, 4, true>(prm, tiles, parts, st);
-    return out8 ? run<false, true, kEpiGrad, 8, false>(prm, grid, 1, st) : run<false, true, kEpiGrad, 4, false>(prm, grid, 1, st);
+    return run<false, true, kEpiGrad, 4, false>(prm, grid, 1, st);
   }
   return run<true, true, kEpiPlain, 4, false>(prm, grid, 1, st);
 }

@@ -278,35 +278,6 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 5) qkv_rope_fwd_kernel(const Q
 // ---------------------------------------------------------------------------------------------
 constexpr int kBwdWarps = 8;
 
-// Codes of two values in a block with a normal scale: tp = x inv + kRoundMagic rounds x inv to an integer, and
-// far keeps the largest distance from it. inv is within 1 ulp of 1 / s, so x inv is within 127 x 2^-23 < 2^-16 of
-// x / s, whose IEEE quotient is within 2^-18 of it: farther than 2^-15 from every tie both round alike
-// (quant_byte's argument with one rounding less, hence half its window).
-__device__ __forceinline__ void code_pair(float x0, float x1, float inv, uint32_t& c0, uint32_t& c1, float& far) {
-  float t0, t1, r0, r1, d0, d1;
-  fma_x2(x0, x1, inv, inv, kRoundMagic, kRoundMagic, t0, t1);
-  fma_x2(t0, t1, -1.0f, -1.0f, kRoundMagic, kRoundMagic, r0, r1);   // minus the integer, exact
-  fma_x2(x0, x1, inv, inv, r0, r1, d0, d1);
-  asm("max.f32 %0, %0, %1, %2;" : "+f"(far) : "f"(fabsf(d0)), "f"(fabsf(d1)));
-  c0 = __float_as_uint(t0);
-  c1 = __float_as_uint(t1);
-}
-
-// Codes of a lane's two chunks with the reciprocals of their blocks' scales: one test for values next to a
-// rounding tie for all 16 (false: a few percent of the warps), after which quant_pack decides.
-__device__ __forceinline__ bool codes16(const float (&y1)[8], const float (&y2)[8], float inv1, float inv2, uint2& w1, uint2& w2) {
-  uint32_t c[8], e[8];
-  float far = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    code_pair(y1[j], y1[j + 1], inv1, c[j], c[j + 1], far);
-    code_pair(y2[j], y2[j + 1], inv2, e[j], e[j + 1], far);
-  }
-  w1 = make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
-  w2 = make_uint2(pack4(e[0], e[1], e[2], e[3]), pack4(e[4], e[5], e[6], e[7]));
-  return far < 0.499969482421875f;   // 0.5 - 2^-15
-}
-
 constexpr int kRing = 3;   // heads of the ring: two on their way while one is at work
 
 // A lane's places in the ring: 16-byte pieces of the gradient's two chunks, then 8 bytes of codes of each.
@@ -487,17 +458,17 @@ __global__ void __launch_bounds__(32 * (G > kBwdWarps ? G : kBwdWarps), G > kBwd
         const BlockQuant bq = block_quant_approx(__uint_as_float(mx[lane & 7]));
         const float inv1 = __shfl_sync(0xffffffffu, bq.inv, c1 >> 2), inv2 = __shfl_sync(0xffffffffu, bq.inv, c2 >> 2);
         const bool plain = __all_sync(0xffffffffu, bq.mode == 2 || (lane & 7) >= nblk);   // normal scales only
-        uint2 o1, o2;
-        if (!codes16(y1, y2, inv1, inv2, o1, o2) || !plain) {
-          uint32_t w[2];
-          quant_pack<8>(y1, block_quant_approx(__uint_as_float(mx[c1 >> 2])), w);
-          o1 = make_uint2(w[0], w[1]);
-          quant_pack<8>(y2, block_quant_approx(__uint_as_float(mx[c2 >> 2])), w);
-          o2 = make_uint2(w[0], w[1]);
+        uint32_t o[4];
+        float far = 0.0f;
+        codes_fast<8>(y1, inv1, o, far);
+        codes_fast<8>(y2, inv2, o + 2, far);
+        if (i < n && (!(far < kFarLimit) || !plain)) {
+          codes_exact<8>(y1, block_quant_approx(__uint_as_float(mx[c1 >> 2])).s, o);
+          codes_exact<8>(y2, block_quant_approx(__uint_as_float(mx[c2 >> 2])).s, o + 2);
         }
         if (i < n) {
-          *reinterpret_cast<uint2*>(dst) = o1;
-          *reinterpret_cast<uint2*>(dst + 8 * (c2 - c1)) = o2;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+          *reinterpret_cast<uint2*>(dst + 8 * (c2 - c1)) = make_uint2(o[2], o[3]);
         }
         if (warp % G == 0 && lane < nblk) a.dx_s[blk + lane] = bq.s;
         dst += a.d;
@@ -534,22 +505,38 @@ __global__ void __launch_bounds__(32 * (G > kBwdWarps ? G : kBwdWarps), G > kBwd
       __syncthreads();                   // before the ring is filled again
     }
   }
+  cudaTriggerProgrammaticLaunchCompletion();
 }
 
-// dgamma[kind][c] = the CTAs' partial sums added in fp64 in a fixed order; one CTA per kind and 32 columns.
-__global__ void __launch_bounds__(256) qkv_dgamma_kernel(const float* __restrict__ part, int ctas, int d,
-                                                         float* __restrict__ dgq, float* __restrict__ dgk) {
-  __shared__ double sum[8][32];
+// CTAs of the backward: at most two for each of 148 SMs, at most one per strip and head.
+constexpr int kQkvBwdMaxCtas = 296;
+
+// dgamma[kind][c] = the CTAs' partial sums added in fp64 in a fixed order; one CTA per kind and 32 columns. A lane
+// has all its loads in flight at once: it waits for memory once (with 8 warps that waited for 37 loads in turn the
+// backward of 8192 tokens took 92 us, 86 so).
+constexpr int kSumWarps = 32;
+constexpr int kSumRows = (kQkvBwdMaxCtas + kSumWarps - 1) / kSumWarps;
+__global__ void __launch_bounds__(32 * kSumWarps) qkv_dgamma_kernel(const float* part, int ctas, int d,
+                                                                    float* __restrict__ dgq, float* __restrict__ dgk) {
+  __shared__ double sum[kSumWarps][32];
   float* out = blockIdx.y == 0 ? dgq : dgk;
   if (out == nullptr) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  float v[kSumRows];
+  cudaGridDependencySynchronize();
+#pragma unroll
+  for (int k = 0; k < kSumRows; ++k) {
+    const int b = warp + k * kSumWarps;
+    v[k] = b < ctas ? part[(int64_t(b) * 2 + blockIdx.y) * d + c] : 0.0f;
+  }
   double t = 0.0;
-  for (int b = warp; b < ctas; b += 8) t += double(part[(int64_t(b) * 2 + blockIdx.y) * d + c]);
+#pragma unroll
+  for (int k = 0; k < kSumRows; ++k) t += double(v[k]);
   sum[warp][lane] = t;
   __syncthreads();
   if (warp == 0) {
 #pragma unroll
-    for (int w = 1; w < 8; ++w) t += sum[w][lane];
+    for (int w = 1; w < kSumWarps; ++w) t += sum[w][lane];
     out[c] = float(t);
   }
 }
@@ -606,8 +593,16 @@ cudaError_t bwd(const QkvRopeArgs& a, int sm_count, cudaStream_t st) {
   qkv_rope_bwd_kernel<T, G, INTER><<<unsigned(ctas), 32 * W, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.part == nullptr) return e;
-  qkv_dgamma_kernel<<<dim3(unsigned(a.d / 32), 2), 256, 0, st>>>(a.part, int(ctas), a.d, a.dgamma_q, a.dgamma_k);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(a.d / 32), 2, 1);
+  cfg.blockDim = dim3(32 * kSumWarps, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, qkv_dgamma_kernel, static_cast<const float*>(a.part), int(ctas), a.d, a.dgamma_q, a.dgamma_k);
 }
 
 template <typename T, bool INTER>
@@ -627,8 +622,6 @@ cudaError_t run(const QkvRopeArgs& a, bool backward, int sm_count, cudaStream_t 
 
 }  // namespace
 
-// CTAs of the backward: at most two for each of 148 SMs, at most one per strip and head.
-constexpr int64_t kQkvBwdMaxCtas = 296;
 int64_t qkv_bwd_ctas(int64_t rows, int64_t hq, int64_t hkv) {
   const int64_t work = rows / 32 * (hq + 2 * hkv);
   return work < kQkvBwdMaxCtas ? (work < 1 ? 1 : work) : kQkvBwdMaxCtas;

@@ -186,4 +186,67 @@ __device__ __forceinline__ float warp_max_nonneg(float m) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 }
 
+// Codes of N values of one block whose scale is normal (or infinite), with inv within 1 ulp of 1 / s:
+// tp = RN(x inv + kRoundMagic) rounds x inv to an integer, and far keeps the largest distance from it (NaN for a
+// NaN). x inv is within 127 x 2^-23 < 2^-16 of x / s, whose IEEE quotient is within 2^-18 of it: where far stays
+// below 0.5 - 2^-15 both round alike (quant_byte's argument with one rounding less, hence half its window).
+constexpr float kFarLimit = 0.499969482421875f;   // 0.5 - 2^-15
+template <int N>
+__device__ __forceinline__ void codes_fast(const float* v, float inv, uint32_t* w, float& far) {
+#pragma unroll
+  for (int k = 0; k < N; k += 4) {
+    float t[4], r[4], d[4];
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      fma_x2(v[k + j], v[k + j + 1], inv, inv, kRoundMagic, kRoundMagic, t[j], t[j + 1]);
+      fma_x2(t[j], t[j + 1], -1.0f, -1.0f, kRoundMagic, kRoundMagic, r[j], r[j + 1]);   // minus the integer, exact
+      fma_x2(v[k + j], v[k + j + 1], inv, inv, r[j], r[j + 1], d[j], d[j + 1]);
+      asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(far) : "f"(fabsf(d[j])), "f"(fabsf(d[j + 1])));
+    }
+    w[k / 4] = pack4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]), __float_as_uint(t[3]));
+  }
+}
+
+// The same codes without a branch per value and for every scale: the IEEE quotient of x and s by Markstein's
+// iteration (IBM J. Res. Dev. 34, 1990): q = RN(x y) with y = RN(1 / s), then q += (x - q s) y twice with fused
+// operations. The first leaves q within 1 ulp of the quotient, so the second remainder is exact and the second
+// sum the correctly rounded quotient. Small scales are brought up by a power of two with their values, so that no
+// remainder loses bits below the subnormals (values under s / 4 may: their code is 0 all the same). Clamped, so
+// that a NaN gets -127 as from quant_byte_exact. An infinite scale gives 0 for finite values.
+template <int N>
+__device__ __forceinline__ void codes_exact(const float* v, float s, uint32_t* w) {
+  const float up = s < 0x1p-60f ? 0x1p100f : 1.0f, us = s * up;
+  const float y = us < INFINITY ? __frcp_rn(us) : 0.0f, ns = us < INFINITY ? -us : 0.0f;
+#pragma unroll
+  for (int k = 0; k < N; k += 4) {
+    float q[4];
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      float x0, x1, r0, r1;
+      mul_x2(v[k + j], v[k + j + 1], up, up, x0, x1);
+      mul_x2(x0, x1, y, y, q[j], q[j + 1]);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        fma_x2(q[j], q[j + 1], ns, ns, x0, x1, r0, r1);
+        fma_x2(r0, r1, y, y, q[j], q[j + 1], q[j], q[j + 1]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = fminf(fmaxf(q[j], -kQMax), kQMax) + kRoundMagic;
+    const uint32_t c = pack4(__float_as_uint(q[0]), __float_as_uint(q[1]), __float_as_uint(q[2]), __float_as_uint(q[3]));
+    w[k / 4] = s == 0.0f ? 0u : c;
+  }
+}
+
+// max |v| of 32 values (NaNs ignored).
+__device__ __forceinline__ float absmax32(const float (&v)[32]) {
+  float m[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      asm("max.f32 %0, %0, %1, %2;" : "+f"(m[k]) : "f"(fabsf(v[i + 2 * k])), "f"(fabsf(v[i + 2 * k + 1])));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
 }  // namespace jf

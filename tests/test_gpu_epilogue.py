@@ -192,6 +192,73 @@ def test_empty_contraction_and_empty_outputs():
     check_status()
 
 
+def _ieee_codes(x):
+    """s = absmax / 127 and the codes RNE(RN(x / s)) in IEEE fp32 on the host; zero blocks get zeros."""
+    M, N = x.shape
+    b = x.cpu().reshape(M // 32, 32, N // 32, 32)
+    s = b.abs().amax(dim=(1, 3)) / torch.tensor(127.0)
+    sb = s[:, None, :, None]
+    q = torch.where(sb == 0, torch.zeros_like(b), (b / torch.where(sb == 0, torch.ones_like(sb), sb)).clamp(-127, 127).round())
+    return q.to(torch.int8).reshape(M, N), s
+
+
+def _tie_dense(g, rows, cols):
+    """Blocks whose values are (n + 1/2) s rounded, up to 3 units in the last place to either side, for scales from
+    the smallest subnormals (where a block's codes may all be 0) to near the largest fp32."""
+    nr, nc = rows // 32, cols // 32
+    e = torch.linspace(-150, 119, nr * nc, device="cuda").reshape(nr, 1, nc, 1)
+    s = ((torch.rand(nr, 1, nc, 1, generator=g, device="cuda") + 1) * torch.exp2(e)).to(torch.float32)
+    s = torch.where(e < -140, torch.exp2(e.double()).to(torch.float32), s)
+    top = (127.0 * s.double()).to(torch.float32)
+    sc = (top.cpu() / torch.tensor(127.0)).cuda()
+    n = torch.randint(-126, 126, (nr, 32, nc, 32), generator=g, device="cuda")
+    x = ((n.double() + 0.5) * sc.double()).to(torch.float32)
+    x = (x.view(torch.int32) + torch.randint(-3, 4, x.shape, generator=g, device="cuda", dtype=torch.int32) * (x.abs() > 1e-44)).view(torch.float32)
+    x = torch.minimum(torch.maximum(x, -top), top)
+    x[:, 0, :, 0] = top[:, 0, :, 0]
+    return x.reshape(rows, cols)
+
+
+def test_codes_next_to_rounding_ties():
+    """The codes of the epilogue and of the QKV gradient are those of the IEEE quotient, for values next to rounding
+    ties and scales over the whole range: the residual alone (an empty contraction, no activation) and values'
+    gradients pass through unchanged before they are quantized."""
+    g = _gen(21)
+    x = _tie_dense(g, 512, 1088)
+    assert torch.isfinite(x).all()
+    q, s = _ieee_codes(x)
+    Y = jf.linear_fwd_epilogue(jf.empty_qtensor(512, 0), jf.empty_qtensor(1088, 0), residual=x)
+    assert torch.equal(Y.s.cpu(), s) and torch.equal(Y.q.cpu(), q)
+    for d in (32, 64, 96, 128, 256):
+        h = 1088 // d - (1088 // d) % 2
+        c = x[:, :h * d].contiguous()
+        q, s = _ieee_codes(c)
+        a = jf.QKVRope(1, 512, 0, h // 2, d)
+        half = h // 2 * d
+        dx, _, _ = jf.qkv_rope_bwd(jf.empty_qtensor(512, h * d), a, None, c[:, :half].reshape(1, 512, h // 2, d), c[:, half:].reshape(1, 512, h // 2, d))
+        assert torch.equal(dx.s.cpu(), s) and torch.equal(dx.q.cpu(), q), d
+    check_status()
+
+
+def test_codes_of_infinities_and_nan():
+    """A NaN leaves its block's scale and the other codes as they are and gets -127; an infinity makes the scale
+    infinite, the finite codes 0 and its own -127."""
+    x = torch.randn(64, 96, generator=_gen(22), device="cuda")
+    y = x.clone()
+    y[3, 5], y[40, 70] = float("nan"), float("inf")
+    W = (jf.empty_qtensor(64, 0), jf.empty_qtensor(96, 0))
+    A, Bq = jf.linear_fwd_epilogue(*W, residual=x), jf.linear_fwd_epilogue(*W, residual=y)
+    clean = x.clone()
+    clean[3, 5] = 0.0
+    q, s = _ieee_codes(clean)
+    q[3, 5] = -127
+    q[32:, 64:] = 0
+    q[40, 70] = -127
+    s[1, 2] = float("inf")
+    assert torch.equal(Bq.q.cpu(), q) and torch.equal(Bq.s.cpu(), s)
+    assert torch.equal(A.q.cpu(), _ieee_codes(x)[0])
+
+
 @pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16, torch.float16])
 def test_strided_rows_in_place_and_guards(dt):
     """The residual stream as columns of a wider buffer, updated in place: the other columns and the rows
