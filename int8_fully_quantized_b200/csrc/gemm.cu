@@ -31,7 +31,7 @@
 //   warps 12-..  output: four or eight warps (Roles) take the finished blocks through the tile's epilogue
 //                (epilogue.cuh) while the next tile is summed.
 // What bounds it (B200, 1965 MHz). Per 128 x 128 tile and contraction block the sum warps of a
-// sub-partition need 256 cycles of FMA pipe (two packed FMAs for 2 elements); measured 445-470 at a
+// sub-partition need 256 cycles of FMA pipe (two packed FMAs for 2 elements); measured 440-465 at a
 // contraction of 16384 and 490 with 8 output warps. The rest is latency the two warps of a sub-partition do
 // not hide for each other (barrier wait, TMEM load 80 cycles) and the hand-off: an MMA's result is visible ~530
 // cycles after its issue, two MMAs' ~620, and each commit holds the tensor pipe for ~57 cycles besides
@@ -83,14 +83,15 @@ constexpr int NUM_SUM_WARPS = 8;    // each owns two 32x32 output blocks of the 
 constexpr int FIRST_OUT_WARP = FIRST_SUM_WARP + NUM_SUM_WARPS;
 // Output warps take the sum warps' blocks through the tile's epilogue: 4 (two sum warps each), or 8 where a
 // tile's epilogue outlasts its main loop (launch_gemm). Registers: the threads start with an equal share;
-// the warpgroup of the producer and the MMA warp gives most of its own up, the sum warps take enough for 64
-// accumulators and 64 partials each, the output warps the rest. The shares' sum must not exceed the launch's
+// the warpgroup of the producer and the MMA warp gives most of its own up, the sum warps take SUM_REGS, enough for
+// 64 accumulators and 64 partials each, the output warps the rest. The shares' sum must not exceed the launch's
 // total, or setmaxnreg would wait for ever.
-template <int NOUT>
+template <int NOUT, int SUM_REGS>
 struct Roles {
   static constexpr int kThreads = 32 * (FIRST_OUT_WARP + NOUT);
-  static constexpr int kCtl = NOUT == 4 ? 40 : 24, kSum = NOUT == 4 ? 168 : 152, kOut = NOUT == 4 ? 136 : 72;
   static constexpr int kLaunch = 65536 / kThreads / 8 * 8;
+  static constexpr int kSum = SUM_REGS, kCtl = NOUT == 8 ? 24 : SUM_REGS > 168 ? 32 : 40;
+  static constexpr int kOut = (kThreads * kLaunch / 128 - kCtl - 2 * kSum) / (NOUT / 4) / 8 * 8;
   static_assert(128 * (kCtl + 2 * kSum) + 32 * NOUT * kOut <= kThreads * kLaunch, "register split");
 };
 constexpr int A_STAGE = BM * KBS * KB;  // 16 KB
@@ -206,8 +207,8 @@ __device__ __forceinline__ float scale_window(const float* __restrict__ base, in
 // order; a part may be empty). The sum warps write each 32 x 32 part into the shared memory of the CTA that
 // owns its block (distributed shared memory: written, not read, as nobody waits for a write; reading the parts
 // from there instead took 6 us more), and the owners' output warps add the parts in rank order.
-template <bool A_MN, bool B_MN, int EPI, int NOUT, bool SPLIT>
-__global__ void __launch_bounds__(Roles<NOUT>::kThreads, 1) gemm_i8_kernel(const __grid_constant__ GemmParams p) {
+template <bool A_MN, bool B_MN, int EPI, int NOUT, int SUM_REGS, bool SPLIT>
+__global__ void __launch_bounds__(Roles<NOUT, SUM_REGS>::kThreads, 1) gemm_i8_kernel(const __grid_constant__ GemmParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem + SMEM_A;
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(Roles<NOUT>::kThreads, 1) gemm_i8_kernel(const
     tmem_alloc(tmem_holder, TMEM_COLS);
     tmem_relinquish();
   }
-  for (int i = threadIdx.x; i < BM * KB / 4; i += Roles<NOUT>::kThreads) reinterpret_cast<uint32_t*>(smem + SMEM_BIAS)[i] = 0x80808080u;
+  for (int i = threadIdx.x; i < BM * KB / 4; i += Roles<NOUT, SUM_REGS>::kThreads) reinterpret_cast<uint32_t*>(smem + SMEM_BIAS)[i] = 0x80808080u;
   fence_proxy_async_smem();   // the bias operand is read by the tensor core
   const cg::cluster_group cluster = cg::this_cluster();
   tc_fence_before();
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(Roles<NOUT>::kThreads, 1) gemm_i8_kernel(const
   const int total_stages = my_tiles * num_kstages;   // this CTA's stages, in order
 
   if (warp < FIRST_SUM_WARP) {
-    setmaxnreg_dec<Roles<NOUT>::kCtl>();
+    setmaxnreg_dec<Roles<NOUT, SUM_REGS>::kCtl>();
     if (warp == 0) {
       // ------------------------------------------------------------------ producer warp
       if (lane == 0) {
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(Roles<NOUT>::kThreads, 1) gemm_i8_kernel(const
     }
   } else if (warp < FIRST_OUT_WARP) {
     // ------------------------------------------------------------------ sum warps
-    setmaxnreg_inc<Roles<NOUT>::kSum>();
+    setmaxnreg_inc<Roles<NOUT, SUM_REGS>::kSum>();
     const int w = warp - FIRST_SUM_WARP;
     const int sub = warp & 3;             // TMEM sub-partition this warp may access = row block in the tile
     const int cb0 = (w >> 2) * 2;         // first of the warp's two column blocks in the tile
@@ -443,8 +444,8 @@ __global__ void __launch_bounds__(Roles<NOUT>::kThreads, 1) gemm_i8_kernel(const
     }
   } else {
     // ------------------------------------------------------------------ output warps
-    if constexpr (Roles<NOUT>::kOut > Roles<NOUT>::kLaunch) setmaxnreg_inc<Roles<NOUT>::kOut>();
-    else setmaxnreg_dec<Roles<NOUT>::kOut>();
+    if constexpr (Roles<NOUT, SUM_REGS>::kOut > Roles<NOUT, SUM_REGS>::kLaunch) setmaxnreg_inc<Roles<NOUT, SUM_REGS>::kOut>();
+    else setmaxnreg_dec<Roles<NOUT, SUM_REGS>::kOut>();
     const int nrb = p.rows >> 5, ncb = p.cols >> 5;
     TileWalk at(p, first_tile, tile_step);
     bool alive = true;
@@ -671,10 +672,10 @@ static bool make_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool A_MN, bool B_MN, int EPI, int NOUT, bool SPLIT>
+template <bool A_MN, bool B_MN, int EPI, int NOUT, int SUM_REGS, bool SPLIT>
 static cudaError_t run(const GemmParams& prm, int grid, int parts, cudaStream_t st) {
   static unsigned long long attr_set = 0;  // one bit per device ordinal
-  auto kern = gemm_i8_kernel<A_MN, B_MN, EPI, NOUT, SPLIT>;
+  auto kern = gemm_i8_kernel<A_MN, B_MN, EPI, NOUT, SUM_REGS, SPLIT>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -687,7 +688,7 @@ static cudaError_t run(const GemmParams& prm, int grid, int parts, cudaStream_t 
   if constexpr (SPLIT) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(grid * parts), 1, 1);
-    cfg.blockDim = dim3(Roles<NOUT>::kThreads, 1, 1);
+    cfg.blockDim = dim3(Roles<NOUT, SUM_REGS>::kThreads, 1, 1);
     cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -698,7 +699,7 @@ static cudaError_t run(const GemmParams& prm, int grid, int parts, cudaStream_t 
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, prm);
   }
-  kern<<<grid, Roles<NOUT>::kThreads, SMEM_BYTES, st>>>(prm);
+  kern<<<grid, Roles<NOUT, SUM_REGS>::kThreads, SMEM_BYTES, st>>>(prm);
   return cudaGetLastError();
 }
 
@@ -775,14 +776,19 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t st) {
     if ((tiles + 5) * c <= sm_count && stages >= (c < 8 ? c : 2 * c)) parts = c;
   prm.share = (stages + parts - 1) / parts;
   if (g.mode == kFwd) {
-    if (parts > 1) return run<false, false, kEpiForward, 4, true>(prm, tiles, parts, st);
-    return out8 ? run<false, false, kEpiForward, 8, false>(prm, grid, 1, st) : run<false, false, kEpiForward, 4, false>(prm, grid, 1, st);
+    if (parts > 1) return run<false, false, kEpiForward, 4, 168, true>(prm, tiles, parts, st);
+    if (out8) return run<false, false, kEpiForward, 8, 152, false>(prm, grid, 1, st);
+    // The register split for the output warps (168) or for the sum warps (176), us: 4096 x 1024 x 4096 with GELU and
+    // both outputs 95 and 101, 4096 x 256 x 4096 75 and 79; 4096 x 2048 x 4096 with GELU 140 and 136,
+    // 8192 x 16384 x 4096 1759 and 1700.
+    return kbn <= 32 ? run<false, false, kEpiForward, 4, 168, false>(prm, grid, 1, st)
+                     : run<false, false, kEpiForward, 4, 176, false>(prm, grid, 1, st);
   }
   if (g.mode == kDgrad) {
-    if (parts > 1) return run<false, true, kEpiGrad, 4, true>(prm, tiles, parts, st);
-    return run<false, true, kEpiGrad, 4, false>(prm, grid, 1, st);
+    if (parts > 1) return run<false, true, kEpiGrad, 4, 176, true>(prm, tiles, parts, st);
+    return run<false, true, kEpiGrad, 4, 176, false>(prm, grid, 1, st);
   }
-  return run<true, true, kEpiPlain, 4, false>(prm, grid, 1, st);
+  return run<true, true, kEpiPlain, 4, 176, false>(prm, grid, 1, st);
 }
 
 cudaError_t launch_gemm_s32(const int8_t* a, const int8_t* b, int32_t* c, int64_t M, int64_t N, int64_t K,
