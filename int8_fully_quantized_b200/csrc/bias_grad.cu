@@ -6,6 +6,8 @@
 // cover a row's 128 bytes), adds its codes exactly in packed 16-bit integers, and multiplies the integer
 // sums by the block's scale into 16 fp32 column sums. Lanes, warps and CTAs (through distributed shared
 // memory) are then added in a fixed order: one launch, no workspace, no atomics, the same bits every time.
+// 8192 x 16384 (135 MB): 29 us with the launch, 4.6 TB/s, where the copy rate would take 20.5; 512 x 1056 8.4 us,
+// a launch with its cluster and the loads' latency.
 #include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>
