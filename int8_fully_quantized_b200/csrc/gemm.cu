@@ -43,11 +43,12 @@
 // index contiguous) straight from their row-major INT8 storage, so dgrad and wgrad re-block along
 // the other axis with no transpose pass.
 //
-// Ordering of the hand-offs: a group is handed back only after tcgen05.wait::ld has returned (its partials
-// are in registers), and it is read only after its MMAs' commit has been observed on the mbarrier, so the
-// barrier instructions themselves order the TMEM accesses; no tcgen05 fence is issued per group (only
-// around the TMEM allocation and release). The two MMAs of a block have one shape and one accumulator,
-// so the tensor core runs them in order.
+// Ordering of the hand-offs: tcgen05 operations of different threads are ordered by a barrier only between
+// tcgen05.fence::before_thread_sync ahead of the arrival (tcgen05.commit implies it) and fence::after_thread_sync
+// behind the wait, so every hand-off of a group carries both: a sum warp that has seen the commit fences before
+// it loads; once its partials are in registers (tcgen05.wait::ld) it fences and its lanes meet before lane 0
+// arrives; the MMA lane fences before it overwrites the group. The two MMAs of a block have one shape and one
+// accumulator, so the tensor core runs them in order.
 //
 // Every mbarrier wait is bounded (ptx.cuh). On a timeout the warp that saw it sets the CTA's abort
 // flag; every other wait then gives up too and the roles end; in-flight copies and MMAs are drained
@@ -334,6 +335,7 @@ __global__ void __launch_bounds__(Roles<NOUT, SUM_REGS>::kThreads, 1) gemm_i8_ke
             if (kk >= nk) break;
             const uint32_t b = uint32_t(gi) & 1u;
             if (!mbar_wait(&tempty[b], (uint32_t(gi >> 1) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
+            tc_fence_after();
             const uint32_t d = tmem_base + b * (GROUP * BN);
             mma_i8(d, bias, bias, bias_idesc, 0u);
             if (kk + 1 < nk) mma_i8(d + BN, bias, bias, bias_idesc, 0u);
@@ -396,7 +398,11 @@ __global__ void __launch_bounds__(Roles<NOUT, SUM_REGS>::kThreads, 1) gemm_i8_ke
           tmem_ld_32x32b_x64(t_base + (b * GROUP + k) * BN, r);
           const float c0 = __shfl_sync(0xffffffffu, cw0, j), c1 = __shfl_sync(0xffffffffu, cw1, j);
           tc_wait_ld64(r);
-          if (last) mbar_arrive_if(&tempty[b], lane == 0);
+          if (last) {
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_if(&tempty[b], lane == 0);
+          }
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             float f0, f1, f2, f3;
@@ -412,6 +418,7 @@ __global__ void __launch_bounds__(Roles<NOUT, SUM_REGS>::kThreads, 1) gemm_i8_ke
           const uint32_t b = uint32_t(gi) & 1u;
           const bool good = mbar_wait_often(&tfull[b], uint32_t(gi >> 1) & 1u, abort_flag, p.status);
           if (!__all_sync(0xffffffffu, good)) { alive = false; break; }
+          tc_fence_after();
           block(b, 0, j0, false);
           block(b, 1, j0 + 1, true);
         }
@@ -419,6 +426,7 @@ __global__ void __launch_bounds__(Roles<NOUT, SUM_REGS>::kThreads, 1) gemm_i8_ke
           const uint32_t b = uint32_t(gi) & 1u;
           const bool good = mbar_wait_often(&tfull[b], uint32_t(gi >> 1) & 1u, abort_flag, p.status);
           alive = __all_sync(0xffffffffu, good);
+          tc_fence_after();
           if (alive) block(b, 0, j0, true);
           ++gi;
         }
@@ -592,6 +600,7 @@ __global__ void __launch_bounds__(S32_THREADS, 1) gemm_i8_s32_kernel(const __gri
       for (int i = 0; ok && i < my_tiles; ++i) {
         const uint32_t buf = uint32_t(i) & 1u;
         if (!mbar_wait(&tempty[buf], (uint32_t(i >> 1) & 1u) ^ 1u, abort_flag, p.status)) break;
+        tc_fence_after();
         for (int ks = 0; ks < num_kstages; ++ks, ++g) {
           const int st = g % S32_STAGES;
           if (!mbar_wait(&full[st], uint32_t(g / S32_STAGES) & 1u, abort_flag, p.status)) { ok = false; break; }
