@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(mx::NUM_THREADS, 1) mxf8_gemm_kernel(const __g
       const uint32_t ph = uint32_t(g / STAGES) & 1u;
       const bool good = mbar_try_wait(&full[st], ph) || mbar_wait(&full[st], ph, abort_flag, p.status);
       if (!__all_sync(0xffffffffu, good)) break;
+      tc_fence_after();   // the MMAs that read the stage's scale columns, whose commit let the producer refill it
       const uint32_t* slot = sSF + st * SF_WORDS;
       const uint32_t col = tmem_base + (uint32_t(32 * q) << 16) + SF_COL0 + uint32_t(st) * 8;
       tmem_st_32x32b_x4(col, slot[lane], slot[32 + lane], slot[64 + lane], slot[96 + lane]);

@@ -68,3 +68,11 @@ def test_hand_offs_are_fenced(name, kernel):
     seq = events(body(name, kernel))
     assert seq.count("wait") >= 2 and seq.count("arrive") >= 1 and "access" in seq
     assert unfenced(seq) == [], seq
+
+
+def test_scale_columns_are_fenced():
+    """The warps that rewrite a stage's scale columns in tensor memory learn from the stage's `full` barrier that the
+    MMAs which read them are done (their commit freed the stage for the producer, whose copies complete `full`)."""
+    text = body("mxfp8.cu", "mxf8_gemm_kernel").replace("&full[", "&sf_full[")
+    seq = events(text)
+    assert unfenced(seq) == [], seq
