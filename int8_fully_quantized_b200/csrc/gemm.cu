@@ -174,7 +174,8 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
 // values per packed instruction, and not as one int -> float conversion per value. Those cost more than
 // their own issue slots: while both sum warps of the MMA warp's sub-partition convert, its tcgen05
 // instructions take 327 cycles each instead of 87.
-constexpr float kSumScale = 8388608.0f;            // 2^23, multiplied into the block's scale (exact)
+constexpr float kSumScale = 8388608.0f;            // 2^23, multiplied into the block's scale
+constexpr float kMaxScaled = 4.0564819207303340848e31f;   // 2^105: below it that multiplication is exact
 __device__ __forceinline__ void partial_x2(uint32_t r0, uint32_t r1, float& f0, float& f1) {
   constexpr float k126 = 8.507059173023461587e37f;   // 2^126
   fma_x2(__uint_as_float(r0), __uint_as_float(r1), k126, k126, -0.0625f, -0.0625f, f0, f1);
@@ -385,8 +386,15 @@ __global__ void __launch_bounds__(Roles<NOUT, SUM_REGS>::kThreads, 1) gemm_i8_ke
 #pragma unroll
       for (int i = 0; i < 32; ++i) acc[0][i] = acc[1][i] = 0.0f;
       for (int w0 = 0; alive && w0 < kblocks; w0 += 32) {
-        // lane l: fp32(sA * sB) of contraction block w0 + l for the warp's two output blocks, times 2^23 (exact)
-        const float cw0 = sa_n * sb0_n * kSumScale, cw1 = sa_n * sb1_n * kSumScale;
+        // lane l: fp32(sA * sB) of contraction block w0 + l for the warp's two output blocks. Times 2^23 that would
+        // pass the largest fp32 from 2^105 on: a window with such a block takes a loop of its own, which multiplies the
+        // partials by 2^23 instead (one test per 32 blocks; the same products and sums, bit for bit).
+        float cw0 = sa_n * sb0_n, cw1 = sa_n * sb1_n;
+        const bool large = !__all_sync(0xffffffffu, fabsf(cw0) < kMaxScaled && fabsf(cw1) < kMaxScaled);
+        if (!large) {
+          cw0 *= kSumScale;
+          cw1 *= kSumScale;
+        }
         const bool more = w0 + 32 < kblocks;   // the rest of this tile, or the start of the next one
         if (!more) at.next();
         load_scales(at, more ? w0 + 32 : 0, more || tile + 1 < my_tiles);
@@ -413,6 +421,40 @@ __global__ void __launch_bounds__(Roles<NOUT, SUM_REGS>::kThreads, 1) gemm_i8_ke
           }
         };
         int j0 = 0;
+        if (__builtin_expect(large, 0)) {
+#pragma unroll 1
+          for (; j0 < nk; j0 += GROUP, ++gi) {
+            const uint32_t b = uint32_t(gi) & 1u;
+            const bool good = mbar_wait_often(&tfull[b], uint32_t(gi >> 1) & 1u, abort_flag, p.status);
+            if (!__all_sync(0xffffffffu, good)) {
+              alive = false;
+              j0 = nk;
+              break;
+            }
+            tc_fence_after();
+            const int n = min(GROUP, nk - j0);
+#pragma unroll 1
+            for (int k = 0; k < n; ++k) {
+              const float c0 = __shfl_sync(0xffffffffu, cw0, j0 + k), c1 = __shfl_sync(0xffffffffu, cw1, j0 + k);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(t_base + (b * GROUP + k) * BN + 32 * h, r);
+                tc_wait_ld(r);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                  float f0, f1;
+                  partial_x2(r[i], r[i + 1], f0, f1);
+                  mul_x2(f0, f1, kSumScale, kSumScale, f0, f1);
+                  fma_x2(h ? c1 : c0, h ? c1 : c0, f0, f1, acc[h][i], acc[h][i + 1], acc[h][i], acc[h][i + 1]);
+                }
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            mbar_arrive_if(&tempty[b], lane == 0);
+          }
+        }
 #pragma unroll 2
         for (; j0 + GROUP <= nk; j0 += GROUP, ++gi) {
           const uint32_t b = uint32_t(gi) & 1u;
