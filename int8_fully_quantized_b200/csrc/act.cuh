@@ -121,11 +121,18 @@ __device__ __forceinline__ float gelu_tanh_f32(float x) {
   return x * rcp_approx(1.0f + exp2_approx(-x * fmaf(kLog2e * kGeluTanhC1, x * x, kLog2e * kGeluTanhC0)));
 }
 
-// act'(x) for x >= 0 of every activation of the linear layers' epilogues, with the approximate functions.
-// GELU: Phi(x) + x phi(x) from erfc_nonneg's fit; the logistic ones from t = exp(-z) <= 1, sigmoid = 1 / (1 + t)
-// and sigmoid (1 - sigmoid) = t / (1 + t)^2. Beyond x = 20 the tanh form's derivative is 1.
-__device__ __forceinline__ float act_grad_pos_f32(float x, int act) {
-  if (act == kActRelu) return x > 0.0f ? 1.0f : 0.0f;
+// act'(x) and act'(-x) for x >= 0 of every activation of the linear layers' epilogues, with the approximate
+// functions. Both sides are formed from the same two small terms, never as 1 minus the other: act'(-x) keeps its
+// relative accuracy where it vanishes (a block of strongly negative pre-activations takes its INT8 scale from it).
+// GELU: Phi(x) + x phi(x) with e = erfc(x / sqrt 2) of erfc_nonneg's fit: 1 - e / 2 + x phi and e / 2 - x phi.
+// The logistic ones, act = x sigmoid(z(x)) with z odd, from t = exp(-z) <= 1, r = 1 / (1 + t) = sigmoid(z) and
+// t r = sigmoid(-z): r + x z' t r^2 and t r - x z' t r^2. Beyond x = 20 the tanh form's are 1 and 0.
+__device__ __forceinline__ void act_grad_pair_epilogue(float x, int act, float& at_pos, float& at_neg) {
+  if (act == kActRelu) {
+    at_pos = x > 0.0f ? 1.0f : 0.0f;
+    at_neg = 0.0f;
+    return;
+  }
   if (act == kActGeluEpi) {
     constexpr float c[10] = {0.17087277f, -0.82215223f, 1.48851587f, -1.13520398f, 0.27886807f,
                              -0.18628806f, 0.09678418f, 0.37409196f, 1.00002368f, -1.26551223f};
@@ -134,8 +141,11 @@ __device__ __forceinline__ float act_grad_pos_f32(float x, int act) {
     float p = c[0];
 #pragma unroll
     for (int i = 1; i < 10; ++i) p = fmaf(p, t, c[i]);
-    const float e = t * exp2_approx(kLog2e * fmaf(-z, z, p));
-    return fmaf(x * 0.39894228040143267794f, exp2_approx(-kLog2e * z * z), fmaf(-0.5f, e, 1.0f));
+    const float h = -0.5f * x;
+    const float e = t * exp2_approx(kLog2e * fmaf(h, x, p)), xphi = x * 0.39894228040143267794f * exp2_approx(kLog2e * h * x);
+    at_pos = fmaf(-0.5f, e, 1.0f) + xphi;
+    at_neg = fmaf(0.5f, e, -xphi);
+    return;
   }
   float z = x, dz = 1.0f;
   if (act == kActGeluTanh) {
@@ -143,8 +153,9 @@ __device__ __forceinline__ float act_grad_pos_f32(float x, int act) {
     z = x * fmaf(kGeluTanhC1, x * x, kGeluTanhC0);
     dz = fmaf(3.0f * kGeluTanhC1, x * x, kGeluTanhC0);
   }
-  const float t = exp2_approx(-kLog2e * z), r = rcp_approx(1.0f + t);
-  return fmaf(x * dz, t * r * r, r);
+  const float t = exp2_approx(-kLog2e * z), r = rcp_approx(1.0f + t), u = t * r;
+  at_pos = fmaf(x * dz, u * r, r);
+  at_neg = fmaf(-x * dz, u * r, u);
 }
 
 }  // namespace jf

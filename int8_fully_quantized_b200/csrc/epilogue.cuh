@@ -190,15 +190,15 @@ __device__ __forceinline__ void activate(float (&v)[32], int act) {
 
 // v *= act'(q s) for one block: a block's pre-activation has at most 256 distinct values, so the warp
 // tabulates act' of all of them in its staging area, indexed by the code's raw byte: 4 evaluations a lane
-// instead of 32, since each serves m and -m (act(x) - act(-x) = x for every activation here, so
-// act'(-x) = 1 - act'(x)).
+// instead of 32, since each serves m and -m.
 __device__ __forceinline__ void times_act_grad(float (&v)[32], const uint32_t (&w)[8], float s, int act, float* tab, int lane) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int m = lane + 1 + 32 * j;   // |code| 1 .. 128
-    const float g = act_grad_pos_f32(float(m) * s, act);
-    if (m < 128) tab[m] = g;
-    tab[256 - m] = s != 0.0f ? 1.0f - g : g;
+    float at_pos, at_neg;
+    act_grad_pair_epilogue(float(m) * s, act, at_pos, at_neg);
+    if (m < 128) tab[m] = at_pos;
+    tab[256 - m] = at_neg;
   }
   if (lane == 0) tab[0] = act == kActRelu ? 0.0f : 0.5f;
   __syncwarp();
