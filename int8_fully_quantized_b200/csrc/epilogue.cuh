@@ -184,7 +184,7 @@ __device__ __forceinline__ void activate(float (&v)[32], int act) {
     for (int i = 0; i < 32; ++i) v[i] = silu_f32(v[i]);
   } else if (act == kActRelu) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = fmaxf(v[i], 0.0f);
+    for (int i = 0; i < 32; ++i) asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(v[i]));   // a NaN stays one
   }
 }
 

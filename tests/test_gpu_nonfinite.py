@@ -1,0 +1,37 @@
+"""Infinities and NaN through the activations of the linear epilogues: they reach the outputs by the activations'
+formulas, so that a diverged product does not turn into ordinary numbers. They enter by the bias (an empty contraction)."""
+import pytest
+import torch
+
+import int8_fully_quantized_b200 as jf
+
+from gpu_common import check_status
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = float("inf"), float("nan")
+
+
+def _forward(act, values, out_dtype=torch.float32, residual=None):
+    bias = torch.linspace(-3, 3, 64, device="cuda")
+    bias[:len(values)] = torch.tensor(values, device="cuda")
+    return jf.linear_fwd_epilogue(jf.empty_qtensor(32, 0), jf.empty_qtensor(64, 0), bias, act, residual, out_dtype=out_dtype)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16, torch.float16])
+def test_relu_of_nan_and_infinities(dt):
+    y = _forward("relu", [NAN, INF, -INF], dt)
+    assert torch.isnan(y[:, 0]).all() and (y[:, 1] == INF).all() and (y[:, 2] == 0).all()
+    assert torch.isfinite(y[:, 3:]).all()
+    r = torch.ones(32, 64, device="cuda", dtype=dt)
+    assert torch.isnan(_forward("relu", [NAN], dt, r)[:, 0]).all()
+    # the codes, by the rules that hold without an activation: a block whose other values are all 0 has scale 0 and
+    # codes 0 (columns 0..31 are not positive); in any other block the NaN gets -127 and the rest is unchanged
+    Y, Z = _forward("relu", [NAN], None), _forward("relu", [0.0], None)
+    assert torch.equal(Y.q, Z.q) and torch.equal(Y.s, Z.s) and not Y.s[:, 0].any()
+    at40 = torch.linspace(-3, 3, 64).tolist()[:40]
+    Y, Z = _forward("relu", at40 + [NAN], None), _forward("relu", at40 + [0.0], None)
+    assert (Y.q[:, 40] == -127).all() and torch.equal(Y.s, Z.s)
+    Z.q[:, 40] = -127
+    assert torch.equal(Y.q, Z.q)
+    check_status()
