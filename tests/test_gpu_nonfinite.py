@@ -35,3 +35,25 @@ def test_relu_of_nan_and_infinities(dt):
     Z.q[:, 40] = -127
     assert torch.equal(Y.q, Z.q)
     check_status()
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16, torch.float16])
+def test_smooth_activations_of_nan_and_infinities(act, dt):
+    """x Phi(x), x sigmoid(z): +inf times 1 is +inf, -inf times 0 and a NaN are NaN."""
+    y = _forward(act, [NAN, INF, -INF], dt)
+    assert torch.isnan(y[:, 0]).all() and (y[:, 1] == INF).all() and torch.isnan(y[:, 2]).all()
+    assert torch.isfinite(y[:, 3:]).all()
+    # the largest finite values stay finite: x for positive, 0 for negative ones
+    big = torch.finfo(torch.float32).max
+    y = _forward(act, [big, -big])
+    assert (y[:, 0] == big).all() and (y[:, 1] == 0).all()
+    check_status()
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu", "relu"])
+def test_infinity_makes_an_infinite_scale(act):
+    """An overflow to +inf shows in the INT8 output as it does without an activation: the block's scale is infinite."""
+    Y = _forward(act, [1.0, INF], None)
+    assert (Y.s[:, 0] == INF).all() and torch.isfinite(Y.s[:, 1]).all()
+    check_status()
