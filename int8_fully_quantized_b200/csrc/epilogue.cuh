@@ -200,7 +200,7 @@ __device__ __forceinline__ void times_act_grad(float (&v)[32], const uint32_t (&
     if (m < 128) tab[m] = at_pos;
     tab[256 - m] = at_neg;
   }
-  if (lane == 0) tab[0] = act == kActRelu ? 0.0f : 0.5f;
+  if (lane == 0) tab[0] = act == kActRelu ? 0.0f : fmaf(0.0f, s, 0.5f);   // NaN for a scale that is not finite
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] *= tab[(w[i >> 2] >> (8 * (i & 3))) & 0xFFu];

@@ -57,3 +57,19 @@ def test_infinity_makes_an_infinite_scale(act):
     Y = _forward(act, [1.0, INF], None)
     assert (Y.s[:, 0] == INF).all() and torch.isfinite(Y.s[:, 1]).all()
     check_status()
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu", "relu"])
+def test_gradient_at_a_block_with_an_infinite_scale(act):
+    """A pre-activation that overflowed leaves a block with an infinite scale, whose codes 0 stand for 0 times infinity: the
+    derivative there is NaN (of ReLU 0, as for every value that is not above 0), not that of an ordinary 0. Blocks with
+    finite scales keep their gradients."""
+    P = jf.QTensor(torch.zeros(32, 64, dtype=torch.int8, device="cuda"), torch.tensor([[INF, 1.0]], device="cuda"))
+    P.q[5, 7] = -127
+    eye = jf.QTensor(torch.eye(64, dtype=torch.int8, device="cuda"), torch.ones(2, 2, device="cuda"))
+    dY = jf.QTensor(torch.ones(32, 64, dtype=torch.int8, device="cuda"), torch.ones(1, 2, device="cuda"))
+    z = jf.linear_dgrad_epilogue(dY, eye, P, act, out_dtype=torch.float32)
+    zero = z[:, :32].flatten()[P.q[:, :32].flatten() == 0]
+    assert (zero == 0).all() if act == "relu" else torch.isnan(zero).all()
+    assert (z[:, 32:] == (0.0 if act == "relu" else 0.5)).all()
+    check_status()
