@@ -29,7 +29,8 @@
 //                window ahead, and are broadcast by warp shuffles. After the last block it leaves its two
 //                fp32 blocks in shared memory (`ofull` / `oempty`) and goes on with the next tile.
 //   warps 12-..  output: four or eight warps (Roles) take the finished blocks through the tile's epilogue
-//                (epilogue.cuh) while the next tile is summed.
+//                (epilogue.cuh) while the next tile is summed. Where there is no next tile, or where it is summed in
+//                less time than the epilogue takes, there are none and the sum warps do it themselves.
 // What bounds it (B200, 1965 MHz). Per 128 x 128 tile and contraction block the sum warps of a
 // sub-partition need 256 cycles of FMA pipe (two packed FMAs for 2 elements); measured 440-465 at a
 // contraction of 16384 and 490 with 8 output warps. The rest is latency the two warps of a sub-partition do
@@ -83,7 +84,7 @@ constexpr int FIRST_SUM_WARP = 4;   // warps 2 and 3 have no role: the sum warps
 constexpr int NUM_SUM_WARPS = 8;    // each owns two 32x32 output blocks of the 128 x 128 tile
 constexpr int FIRST_OUT_WARP = FIRST_SUM_WARP + NUM_SUM_WARPS;
 // Output warps take the sum warps' blocks through the tile's epilogue: 4 (two sum warps each), or 8 where a
-// tile's epilogue outlasts its main loop (launch_gemm). Registers: the threads start with an equal share;
+// tile's epilogue outlasts its main loop, or 0: each sum warp its own (launch_gemm). Registers: the threads start with an equal share;
 // the warpgroup of the producer and the MMA warp gives most of its own up, the sum warps take SUM_REGS, enough for
 // 64 accumulators and 64 partials each, the output warps the rest. The shares' sum must not exceed the launch's
 // total, or setmaxnreg would wait for ever.
@@ -91,8 +92,8 @@ template <int NOUT, int SUM_REGS>
 struct Roles {
   static constexpr int kThreads = 32 * (FIRST_OUT_WARP + NOUT);
   static constexpr int kLaunch = 65536 / kThreads / 8 * 8;
-  static constexpr int kSum = SUM_REGS, kCtl = NOUT == 8 ? 24 : SUM_REGS > 168 ? 32 : 40;
-  static constexpr int kOut = (kThreads * kLaunch / 128 - kCtl - 2 * kSum) / (NOUT / 4) / 8 * 8;
+  static constexpr int kSum = SUM_REGS, kCtl = NOUT == 8 ? 24 : NOUT == 4 && SUM_REGS > 168 ? 32 : 40;
+  static constexpr int kOut = NOUT == 0 ? 0 : (kThreads * kLaunch / 128 - kCtl - 2 * kSum) / (NOUT == 0 ? 1 : NOUT / 4) / 8 * 8;
   static_assert(128 * (kCtl + 2 * kSum) + 32 * NOUT * kOut <= kThreads * kLaunch, "register split");
 };
 constexpr int A_STAGE = BM * KBS * KB;  // 16 KB
@@ -378,10 +379,10 @@ __global__ void __launch_bounds__(Roles<NOUT, SUM_REGS>::kThreads, 1) gemm_i8_ke
     };
     TileWalk at(p, first_tile, tile_step);                       // the tile of the scales loaded last
     load_scales(at, 0, my_tiles > 0);
-    const int row_blk0 = at.row() * (BM / 32), col_blk0 = at.col() * (BN / 32);   // the first tile's blocks
     int gi = 0;                           // groups consumed so far
     bool alive = true;
     for (int tile = 0; tile < my_tiles; ++tile) {
+      const int rbk = at.row() * (BM / 32) + sub, cbk = at.col() * (BN / 32) + cb0;   // the tile's (`at` moves on below)
       float acc[2][32];
 #pragma unroll
       for (int i = 0; i < 32; ++i) acc[0][i] = acc[1][i] = 0.0f;
@@ -479,10 +480,21 @@ __global__ void __launch_bounds__(Roles<NOUT, SUM_REGS>::kThreads, 1) gemm_i8_ke
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int b = 2 * w + h, owner = b & (parts - 1);
-          if (row_blk0 + sub < nrb && col_blk0 + cb0 + h < ncb)
+          if (rbk < nrb && cbk + h < ncb)
             block_to_smem(acc[h], cluster.map_shared_rank(smem + SMEM_OUT + (b - owner + rank) * 4096, owner), lane);
         }
         break;
+      }
+      if constexpr (NOUT == 0) {
+        if (kblocks == 0) at.next();      // no scales of the next tile were loaded
+        const int nblk = rbk < nrb ? min(2, ncb - cbk) : 0;
+#pragma unroll 1
+        for (int h = 0; h < nblk; ++h) {
+          block_epilogue<EPI>(p.ep, acc[0], rbk, cbk + h, ncb, smem + SMEM_OUT + (2 * w + h) * 4096, lane);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[0][i] = acc[1][i];
+        }
+        continue;
       }
       // the finished blocks to the output warps, and on to the next tile
       const bool room = mbar_wait_often(&oempty[w], (uint32_t(tile) & 1u) ^ 1u, abort_flag, p.status);
@@ -492,7 +504,7 @@ __global__ void __launch_bounds__(Roles<NOUT, SUM_REGS>::kThreads, 1) gemm_i8_ke
       __syncwarp();
       if (lane == 0) mbar_arrive(&ofull[w]);
     }
-  } else {
+  } else if constexpr (NOUT > 0) {
     // ------------------------------------------------------------------ output warps
     if constexpr (Roles<NOUT, SUM_REGS>::kOut > Roles<NOUT, SUM_REGS>::kLaunch) setmaxnreg_inc<Roles<NOUT, SUM_REGS>::kOut>();
     else setmaxnreg_dec<Roles<NOUT, SUM_REGS>::kOut>();
@@ -810,9 +822,8 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t st) {
   prm.ep.y_type = g.y_type;
   prm.ep.y_ld = g.y_ld * bytes(g.y_type);
   // The exact GELU (an erfc per element) takes 4 output warps longer than 64 contraction blocks take the sum warps:
-  // up to there 8 of them are faster (4096 x 1024 x 4096 119 us against 131, 4096 x 2048 x 4096 154 against 160),
-  // beyond they only slow the sum warps down. Every other epilogue keeps up with 4 (4096 x 1024 x 4096 with GELU
-  // and both outputs 92 us against 98).
+  // up to there 8 of them are faster (4096 x 2048 x 4096 154 us against 160), beyond they only slow the sum warps down.
+  // Every other epilogue keeps up with 4.
   const bool out8 = g.act == kActGelu && kbn <= 64;
   // Few tiles leave SMs idle: the contraction is then split over clusters of 2, 4 or 8 CTAs, each with at least
   // one pipeline stage (two in clusters of 8, where one costs 1 us more than clusters of 4), as long as all
@@ -826,8 +837,21 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t st) {
   for (int c = 2; g.split_ok && c <= 8; c *= 2)
     if ((tiles + 5) * c <= sm_count && stages >= (c < 8 ? c : 2 * c)) parts = c;
   prm.share = (stages + parts - 1) / parts;
+  // The sum warps as output warps (`direct`): output warps pay for overlapping a tile's epilogue with the next tile, by
+  // a copy through shared memory and cold code at a call's end, and 4 of them take twice as long as 8 for one epilogue.
+  // With and without them, us in a graph of such calls, INT8 out: one tile a CTA, 128^3 8.5 and 5.8, 512^3 11.2 and
+  // 8.7, 1024^3 with GELU (jf_linear_fwd_gelu) 21.0 and 17.6, 1024 x 4096 x 1024 38.1 and 36.3; more tiles,
+  // 4096 x 32 x 4096 30.2 and 17.9, 4096 x 256 x 4096 36.2 and 28.7 (weight gradient 29.6 and 29.0, but 29.4 and 34.5 with
+  // fp32 out, whose border is 128: 26.6 and 26.1), 4096 x 512 x 4096 as input gradient 42.0 and 42.0; the exact GELU
+  // 4096 x 1024 x 4096 109 and 104, 4096 x 2048 x 4096 152 and 158.
+  const bool direct = parts == 1 && (tiles <= sm_count || kbn <= (g.y == nullptr ? 8 : 4) || (g.act == kActGelu && kbn <= 32));
+  // without bias, activation and residual the instance without their code (cold: 128^3 6.4 with it, 5.8 without)
+  const bool plain = g.bias == nullptr && g.act == kActNone && g.res == nullptr && g.pre_q == nullptr;
   if (g.mode == kFwd) {
     if (parts > 1) return run<false, false, kEpiForward, 4, 168, true>(prm, tiles, parts, st);
+    if (direct)
+      return plain ? run<false, false, kEpiPlain, 0, 232, false>(prm, grid, 1, st)
+                   : run<false, false, kEpiForward, 0, 232, false>(prm, grid, 1, st);
     if (out8) return run<false, false, kEpiForward, 8, 152, false>(prm, grid, 1, st);
     // The register split for the output warps (168) or for the sum warps (176), us: 4096 x 1024 x 4096 with GELU and
     // both outputs 95 and 101, 4096 x 256 x 4096 75 and 79; 4096 x 2048 x 4096 with GELU 140 and 136,
@@ -837,8 +861,12 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t st) {
   }
   if (g.mode == kDgrad) {
     if (parts > 1) return run<false, true, kEpiGrad, 4, 176, true>(prm, tiles, parts, st);
+    if (direct)
+      return plain ? run<false, true, kEpiPlain, 0, 232, false>(prm, grid, 1, st)
+                   : run<false, true, kEpiGrad, 0, 232, false>(prm, grid, 1, st);
     return run<false, true, kEpiGrad, 4, 176, false>(prm, grid, 1, st);
   }
+  if (direct) return run<true, true, kEpiPlain, 0, 232, false>(prm, grid, 1, st);
   return run<true, true, kEpiPlain, 4, 176, false>(prm, grid, 1, st);
 }
 
