@@ -286,8 +286,8 @@ __global__ void __launch_bounds__(Roles<NOUT, SUM_REGS>::kThreads, 1) gemm_i8_ke
         for (int g = 0; g < total_stages; ++g) {
           const int row0 = at.row() * BM, col0 = at.col() * BN;
           // far ahead of the MMAs: it looks now and then instead of polling beside the warps at work
-          for (int i = 0; i < 4096 && !mbar_try_wait(&empty[st], ph ^ 1u); ++i) __nanosleep(300);
-          if (!mbar_wait(&empty[st], ph ^ 1u, abort_flag, p.status)) break;
+          for (int i = 0; i < 4096 && !mbar_try_wait<true>(&empty[st], ph ^ 1u); ++i) __nanosleep(300);
+          if (!mbar_wait<true>(&empty[st], ph ^ 1u, abort_flag, p.status)) break;
           mbar_arrive_expect_tx(&full[st], A_STAGE + B_STAGE);
           pending |= 1u << st;
           pend_ph = (pend_ph & ~(1u << st)) | (ph << st);
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(Roles<NOUT, SUM_REGS>::kThreads, 1) gemm_i8_ke
         }
         // Teardown: every copy issued has landed before the CTA exits.
         for (int s = 0; s < STAGES; ++s)
-          if (pending & (1u << s)) mbar_wait_teardown(&full[s], (pend_ph >> s) & 1u, p.status);
+          if (pending & (1u << s)) mbar_wait_teardown<true>(&full[s], (pend_ph >> s) & 1u, p.status);
       }
       __syncwarp();
     } else if (warp == MMA_WARP) {
@@ -329,14 +329,14 @@ __global__ void __launch_bounds__(Roles<NOUT, SUM_REGS>::kThreads, 1) gemm_i8_ke
         int gi = 0, slot = 0, left = kblocks;       // groups so far: group gi lives in TMEM half gi % 2
         uint32_t sph = 0;
         for (int s = 0; ok && s < total_stages; ++s) {
-          if (!mbar_wait(&full[slot], sph, abort_flag, p.status)) break;
+          if (!mbar_wait<true>(&full[slot], sph, abort_flag, p.status)) break;
           const int nk = min(KBS, left);
           uint32_t a = a_lo + slot * (A_STAGE / 16), bb = b_lo + slot * (B_STAGE / 16);
 #pragma unroll
           for (int kk = 0; kk < KBS; kk += GROUP) {
             if (kk >= nk) break;
             const uint32_t b = uint32_t(gi) & 1u;
-            if (!mbar_wait(&tempty[b], (uint32_t(gi >> 1) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
+            if (!mbar_wait<true>(&tempty[b], (uint32_t(gi >> 1) & 1u) ^ 1u, abort_flag, p.status)) { ok = false; break; }
             tc_fence_after();
             const uint32_t d = tmem_base + b * (GROUP * BN);
             mma_i8(d, bias, bias, bias_idesc, 0u);
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(Roles<NOUT, SUM_REGS>::kThreads, 1) gemm_i8_ke
         // Teardown: no MMA may still be writing TMEM when it is freed.
         if (issued) {
           tc_commit(drain);
-          mbar_wait_teardown(drain, 0u, p.status);
+          mbar_wait_teardown<true>(drain, 0u, p.status);
         }
       }
       __syncwarp();

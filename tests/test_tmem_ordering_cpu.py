@@ -11,7 +11,7 @@ from int8_fully_quantized_b200 import build_lib
 # accumulator (and scale-column) barriers; `full` / `empty` of the shared-memory ring order no tensor memory
 BARRIERS = r"(?:tfull|tempty|acc_full|acc_empty|sf_full)"
 EVENTS = [
-    ("wait", re.compile(r"\bmbar_(?:try_)?wait(?:_often)?\(\s*&" + BARRIERS + r"\[")),
+    ("wait", re.compile(r"\bmbar_(?:try_)?wait(?:_often)?(?:<\w+>)?\(\s*&" + BARRIERS + r"\[")),
     ("arrive", re.compile(r"\bmbar_arrive(?:_if)?\(\s*&" + BARRIERS + r"\[")),
     ("after", re.compile(r"\btc_fence_after\(")),
     ("before", re.compile(r"\btc_fence_before\(")),
