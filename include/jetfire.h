@@ -248,7 +248,8 @@ JF_API int jf_layernorm_i8_bwd_noalloc(jf_cqtensor X, jf_cqtensor dY, const floa
  * ------------------------------------------------------------------------------------------------ */
 
 /* Activations: RELU max(x, 0); GELU x Phi(x); GELU_TANH 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3)));
- * SILU x / (1 + exp(-x)). The derivative of RELU at 0 is taken as 0. */
+ * SILU x / (1 + exp(-x)). The derivative of RELU at 0 is taken as 0. NaN and infinities go through by these formulas:
+ * +infinity stays (and makes its block's scale infinite), -infinity becomes NaN in all but RELU, a NaN stays one. */
 typedef enum { JF_ACT_NONE = 0, JF_ACT_RELU = 1, JF_ACT_GELU = 2, JF_ACT_GELU_TANH = 3, JF_ACT_SILU = 4 } jf_activation;
 
 /* Dense row-major matrices whose rows start ld elements apart (device pointers; p = NULL: absent).

@@ -1,13 +1,14 @@
 // Bias gradient of an INT8 linear layer: db[n] = sum over the rows m of fp32(dY.q[m, n]) * dY.s[m/32, n/32].
 //
-// One pass over the codes (1 byte and 1/256 of a scale per element; the output is negligible), so HBM
-// bounds it. A cluster of up to 8 CTAs owns a slab of 128 columns; its warps take the slab's 32-row
+// One pass over the codes (1 byte and 1/256 of a scale per element; the output is negligible): HBM sets the
+// floor. A cluster of up to 8 CTAs owns a slab of 128 columns; its warps take the slab's 32-row
 // blocks in turn. Of one block a lane reads 16 columns of 8 rows (8 independent 16-byte loads; 8 lanes
 // cover a row's 128 bytes), adds its codes exactly in packed 16-bit integers, and multiplies the integer
 // sums by the block's scale into 16 fp32 column sums. Lanes, warps and CTAs (through distributed shared
 // memory) are then added in a fixed order: one launch, no workspace, no atomics, the same bits every time.
-// 8192 x 16384 (135 MB): 29 us with the launch, 4.6 TB/s, where the copy rate would take 20.5; 512 x 1056 8.4 us,
-// a launch with its cluster and the loads' latency.
+// 8192 x 16384 (135 MB): 29-33 us with the launch, where the copy rate would take 20.5. DRAM is at 52% under ncu and the
+// warps wait for loads (long scoreboard 11.8): 1024 CTAs at 4 an SM are 1.73 waves, and a warp loads its next block only
+// after it has summed the present one. 512 x 1056 8.4 us, a launch with its cluster and the loads' latency.
 #include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>

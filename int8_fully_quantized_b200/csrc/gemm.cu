@@ -40,6 +40,11 @@
 // groups of two, 473 with four of one) and why every thread of a sum warp polls the barrier itself (one
 // polling lane and a warp synchronization: 492). The main loop is unrolled by four blocks: rolled, branches
 // and instruction fetch cost 9% more.
+// At a contraction of 1024 (4096 x 1024 x 4096, 7 tiles a CTA; clock64 of CTA 0) the sum warps need 485 cycles a block in
+// the plain forward and 590-600 beside output warps with GELU and two INT8 outputs (or GELU'), which take 20500 cycles
+// for a tile's 4 blocks a warp and so set the pace together with the sum warps (19300 a tile). A tile's end costs
+// 850-1250 cycles, the start up to the first sum 3100-3500, the last tile's epilogue 6400 (plain) or 15000, of
+// 128000 and 158000 in all.
 // Operand orientation: A and B are read K-major (contraction contiguous) or MN-major (output
 // index contiguous) straight from their row-major INT8 storage, so dgrad and wgrad re-block along
 // the other axis with no transpose pass.
@@ -84,10 +89,11 @@ constexpr int FIRST_SUM_WARP = 4;   // warps 2 and 3 have no role: the sum warps
 constexpr int NUM_SUM_WARPS = 8;    // each owns two 32x32 output blocks of the 128 x 128 tile
 constexpr int FIRST_OUT_WARP = FIRST_SUM_WARP + NUM_SUM_WARPS;
 // Output warps take the sum warps' blocks through the tile's epilogue: 4 (two sum warps each), or 8 where a
-// tile's epilogue outlasts its main loop, or 0: each sum warp its own (launch_gemm). Registers: the threads start with an equal share;
-// the warpgroup of the producer and the MMA warp gives most of its own up, the sum warps take SUM_REGS, enough for
+// tile's epilogue outlasts its main loop, or 0: each sum warp its own (launch_gemm). Registers: the threads start
+// with an equal share; the warpgroup of the producer and the MMA warp gives most of its own up, the sum warps take SUM_REGS, enough for
 // 64 accumulators and 64 partials each, the output warps the rest. The shares' sum must not exceed the launch's
-// total, or setmaxnreg would wait for ever.
+// total, or setmaxnreg would wait for ever. What ptxas stores to the stack all the same: 180 bytes a thread with
+// eight output warps (72 registers each), 4-28 in the forwards' other instances and in those without output warps.
 template <int NOUT, int SUM_REGS>
 struct Roles {
   static constexpr int kThreads = 32 * (FIRST_OUT_WARP + NOUT);
@@ -853,9 +859,8 @@ cudaError_t launch_gemm(const GemmArgs& g, int sm_count, cudaStream_t st) {
       return plain ? run<false, false, kEpiPlain, 0, 232, false>(prm, grid, 1, st)
                    : run<false, false, kEpiForward, 0, 232, false>(prm, grid, 1, st);
     if (out8) return run<false, false, kEpiForward, 8, 152, false>(prm, grid, 1, st);
-    // The register split for the output warps (168) or for the sum warps (176), us: 4096 x 1024 x 4096 with GELU and
-    // both outputs 95 and 101, 4096 x 256 x 4096 75 and 79; 4096 x 2048 x 4096 with GELU 140 and 136,
-    // 8192 x 16384 x 4096 1759 and 1700.
+    // The register split for the output warps (168) or for the sum warps (176): 4096 x 1024 x 4096 with GELU and both
+    // outputs takes 6% longer with 176, 4096 x 2048 x 4096 with GELU 3% longer with 168 and 8192 x 16384 x 4096 3.5%.
     return kbn <= 32 ? run<false, false, kEpiForward, 4, 168, false>(prm, grid, 1, st)
                      : run<false, false, kEpiForward, 4, 176, false>(prm, grid, 1, st);
   }

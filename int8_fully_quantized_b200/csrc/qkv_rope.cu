@@ -181,8 +181,10 @@ __device__ __forceinline__ float sumsq8(const uint2& w) { return float(__dp4a(in
 // ---------------------------------------------------------------------------------------------
 // Forward: 1 byte read and sizeof(T) bytes written per element. A warp takes 32 / G tokens and a range of the heads
 // (blockIdx.y). 8192 tokens of 32 + 8 heads of 128 with norms to bf16 (151 MB): 34.8 us, 4.4 TB/s including the
-// launch; 152 MB at the copy rate would take 23. Bound by loads in flight (92 registers, 5 CTAs an SM) and the issue
-// slots (61% busy) together: codes of 4 heads ahead beat 1 ahead at 8 CTAs (45 us) and 4 CTAs (38.9).
+// launch; 152 MB at the copy rate would take 23. Neither DRAM (34% under ncu) nor the issue slots (61%) are full:
+// latency bounds it. The codes of 4 heads wait in registers (92, so 5 CTAs an SM), and none are on their way while those
+// are worked on; 1 head ahead at 8 CTAs (45 us) and 4 CTAs (38.9) are slower. A ring in shared memory as in the backward
+// would hold them without registers (not tried here).
 // ---------------------------------------------------------------------------------------------
 constexpr int kFwdWarps = 4;
 constexpr int kAhead = 4;
@@ -277,9 +279,10 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 5) qkv_rope_fwd_kernel(const Q
 // flight take no registers. The slots of a persistent grid share the strips and heads of one kind evenly,
 // each a contiguous range; the weights' gradients stay in registers while the kind lasts and are then added
 // into the CTA's row of the workspace; a second kernel adds the rows in a fixed order in fp64.
-// What bounds it: 470 instructions per 16 values at 57% of the issue slots with 16 warps an SM (128 registers), not
-// the 195 MB: 8192 tokens of 32 + 8 heads of 128 with norms in 83 us, where the copy rate allows 30 (without norms 60
-// of 23). Tried and slower: two tokens a lane (spills, 172 us), 3 CTAs an SM (135), angles and gamma re-read per
+// What bounds it: latency between 470 instructions per 16 values, at 57% of the issue slots with 16 warps an SM (128
+// registers; the half-layout instances store up to 16 bytes a thread to the stack), not the 195 MB (DRAM 27%). The
+// instance serves norm, no norm and values alike, so calls without a norm carry its registers. 8192 tokens of 32 + 8
+// heads of 128 with norms in 83 us, where the copy rate allows 30 (without norms 60 of 23). Tried and slower: two tokens a lane (spills, 172 us), 3 CTAs an SM (135), angles and gamma re-read per
 // head (139) or gamma from shared memory (96), a slot's heads dealt out in turn instead of in ranges (116), a branch
 // to the quotient per 8 values (98).
 // ---------------------------------------------------------------------------------------------
@@ -520,7 +523,7 @@ constexpr int kQkvBwdMaxCtas = 296;
 
 // dgamma[kind][c] = the CTAs' partial sums added in fp64 in a fixed order; one CTA per kind and 32 columns. A lane
 // has all its loads in flight at once: it waits for memory once (with 8 warps that waited for 37 loads in turn the
-// backward of 8192 tokens took 92 us, 86 so).
+// backward of 8192 tokens took 6 us longer).
 constexpr int kSumWarps = 32;
 constexpr int kSumRows = (kQkvBwdMaxCtas + kSumWarps - 1) / kSumWarps;
 __global__ void __launch_bounds__(32 * kSumWarps) qkv_dgamma_kernel(const float* part, int ctas, int d,
@@ -574,8 +577,8 @@ cudaError_t fwd(const QkvRopeArgs& a, int sm_count, cudaStream_t st) {
   const int64_t gx = (a.tokens + kFwdWarps * (32 / G) - 1) / (kFwdWarps * (32 / G));
   // One head a warp while all CTAs run at once (64 tokens of 32 + 8 heads of 128: 7.2 us, with 4 heads 9.2). Beyond
   // that whole groups of kAhead heads, whose loads a warp has in flight together (2048 tokens 15.4 us, with two
-  // heads 19.4; 512 tokens 9.1 and 11.2), more of them the more tokens there are (8192 tokens 12 heads 37.8 us,
-  // 4 heads 42.0): the angles are loaded once a warp.
+  // heads 19.4; 512 tokens 9.1 and 11.2), more of them the more tokens there are (8192 tokens: 4 heads a warp take 11%
+  // longer than 12): the angles are loaded once a warp.
   int64_t per = 1;
   if (gx * heads > int64_t(sm_count) * 5) {
     per = (gx * heads / (int64_t(sm_count) * 16) + kAhead - 1) / kAhead * kAhead;
