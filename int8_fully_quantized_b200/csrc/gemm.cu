@@ -32,8 +32,8 @@
 //                (epilogue.cuh) while the next tile is summed. Where there is no next tile, or where it is summed in
 //                less time than the epilogue takes, there are none and the sum warps do it themselves.
 // What bounds it (B200, 1965 MHz). Per 128 x 128 tile and contraction block the sum warps of a
-// sub-partition need 256 cycles of FMA pipe (two packed FMAs for 2 elements); measured 440-465 at a
-// contraction of 16384 and 490 with 8 output warps. The rest is latency the two warps of a sub-partition do
+// sub-partition need 256 cycles of FMA pipe (two packed FMAs for 2 elements); measured 470 at a
+// contraction of 16384 and 490 at 4096. The rest is latency the two warps of a sub-partition do
 // not hide for each other (barrier wait, TMEM load 80 cycles) and the hand-off: an MMA's result is visible ~530
 // cycles after its issue, two MMAs' ~620, and each commit holds the tensor pipe for ~57 cycles besides
 // an MMA's 64, which is why two blocks share one commit (389 cycles per block in a reduced kernel with two
